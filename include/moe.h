@@ -333,6 +333,162 @@ int moe_backward_saved(const moe_shape* shape, const moe_weights* w, const int32
                        const void* train_workspace, size_t train_ws_bytes, void* workspace,
                        size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Products, adapters and updates next to the layer.  The conventions above
+ * hold: contiguous row-major device tensors, 16-byte aligned pointers (4-byte
+ * where said), the caller's stream and buffers, host checks before the first
+ * launch, no host synchronisation, no memory kept between calls.  Outputs
+ * must not overlap inputs, the workspace or each other.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of outputs (any other value: MOE_ERR_INVALID_ARG) */
+#define MOE_DTYPE_F32 0
+#define MOE_DTYPE_BF16 1
+
+/* moe_gemm_shape.weight_layout (any other value: MOE_ERR_INVALID_ARG) */
+#define MOE_LAYOUT_NK 0 /* w [G, N, K]: row n of a group holds output column n's weights */
+#define MOE_LAYOUT_KN 1 /* w [G, K, N]: the transposed storage (bf16 only) */
+
+/*
+ * Grouped products with ragged row groups: the expert products of the layer
+ * without its routing, SwiGLU and tile padding ("Mixture of Experts optimiza
+ * Transformers y LLMs", section "Ejecución eficiente: backends de expertos":
+ * rows sorted by expert id meet the stacked expert weights), for experts with
+ * another activation and for rows that arrive grouped from an expert-parallel
+ * exchange.
+ *   y[r][n] = sum_k x[r][k] * w[g][n][k]   (MOE_LAYOUT_NK)
+ *   y[r][n] = sum_k x[r][k] * w[g][k][n]   (MOE_LAYOUT_KN)
+ * for every row r with offsets[g] <= r < offsets[g + 1].  With the weights of a
+ * MOE_LAYOUT_NK call of width N, K, a MOE_LAYOUT_KN call of width K, N turns
+ * dy into the gradient of x.
+ *   x        bf16 [R, K]
+ *   offsets  device int32 [G + 1], ascending, in [0, R] (moe_align's offsets, or its
+ *            padded_offsets for block_m = 1).  Read on the device and clamped there:
+ *            values outside [0, R] and descending pairs give empty or cut groups, never
+ *            accesses outside the tensors; overlapping groups give undefined values.
+ *   w        bf16, or E4M3 codes [G, N, K] with w_scale fp32 [G, N] (4-byte aligned):
+ *            weight = value(code) * w_scale[g][n]  (MOE_LAYOUT_NK only)
+ *   y        [R, N], fp32 or bf16 (out_dtype; one rounding of the fp32 sum).  Rows
+ *            before offsets[0] and from offsets[G] on are left as they were, and
+ *            those rows of x are not read.
+ *   workspace  device buffer of ws_bytes >= moe_grouped_gemm_workspace_size(shape)
+ *            (NULL when that is 0)
+ * Limits: 0 <= R, 1 <= G <= 256, N and K positive multiples of 8, N * K * 2 < 2^31,
+ * 288 * 4 * max(N, K) < 2^31, R + 256 * 257 < 2^31, (R / 256 + 2 G) (N / 64 + 1) < 2^23.
+ * R == 0 does nothing.  Products of bf16 values are exact, sums fp32 in a
+ * fixed order: the same call gives bitwise the same rows.
+ */
+typedef struct moe_gemm_shape {
+  int32_t R;             /* rows of x and y */
+  int32_t G;             /* groups (experts) */
+  int32_t N;             /* width of y */
+  int32_t K;             /* width of x */
+  int32_t weight_format; /* MOE_WEIGHTS_* */
+  int32_t weight_layout; /* MOE_LAYOUT_* */
+  int32_t out_dtype;     /* MOE_DTYPE_* of y */
+} moe_gemm_shape;
+
+int moe_grouped_gemm_workspace_size(const moe_gemm_shape* shape, size_t* bytes);
+int moe_grouped_gemm(const moe_gemm_shape* shape, const void* x, const int32_t* offsets,
+                     const void* w, const float* w_scale, void* y, void* workspace,
+                     size_t ws_bytes, void* stream);
+
+/*
+ * The weight gradient of moe_grouped_gemm (MOE_LAYOUT_NK):
+ *   dw[g][n][k] = sum over offsets[g] <= r < offsets[g + 1] of dy[r][n] * x[r][k]
+ * dy bf16 [R, N], x bf16 [R, K], dw fp32 [G, N, K] (overwritten; groups without
+ * rows get zeros, also for R == 0).  offsets as above.  weight_format,
+ * weight_layout and out_dtype must be 0.  Limits as above, and R * max(N, K) *
+ * 2 < 2^31, N * K * 4 < 2^31.
+ */
+int moe_grouped_gemm_wgrad(const moe_gemm_shape* shape, const void* dy, const void* x,
+                           const int32_t* offsets, float* dw, void* stream);
+
+/*
+ * Low-rank adapters of many requests beside one shared projection ("Transformers
+ * v5 El Secreto Detrás de los Modelos MoE Más Rápidos", section "Entrenamiento
+ * MoE": adapters on grouped kernels):
+ *   y[t] = W x[t] + scale[a] * B[a] (A[a] x[t]),   a = adapter[t]
+ *   y[t] = W x[t]                                   for a < 0 or a >= L (no adapter)
+ *   x        bf16 [T, D]
+ *   w        bf16 [N, D]      the shared projection
+ *   lora_a   bf16 [L, r, D]   lora_b bf16 [L, N, r]
+ *   adapter  device int32 [T], rows in any order (4-byte aligned)
+ *   scale    fp32 [L] (4-byte aligned), or NULL: 1 for every adapter
+ *   y        [T, N], fp32 or bf16 (out_dtype)
+ *   xa       fp32 [T, r] out, or NULL: A[a] x[t] before the scale (zero rows without
+ *            an adapter), which moe_lora_backward takes
+ * A[a] x is summed in fp32 and enters the second product as two bf16 parts (16 bits
+ * of it); everything else as the layer's products.  Adapters no row names are not
+ * read, and an adapter's values reach the rows that name it only.
+ * Limits: 0 <= T, 1 <= L <= 65536, 8 <= r <= 128, D, N and r multiples of 8,
+ * N * D * 2 < 2^31, 288 * 4 * max(N, D) < 2^31, T <= 2^24,
+ * (T / 256 + 1) (max(N, D) / 64 + 1) < 2^23.
+ */
+typedef struct moe_lora_shape {
+  int32_t T;         /* rows (tokens) */
+  int32_t D;         /* width of x */
+  int32_t N;         /* width of y */
+  int32_t L;         /* adapters */
+  int32_t r;         /* rank */
+  int32_t out_dtype; /* MOE_DTYPE_* of y (forward) or dx (backward) */
+} moe_lora_shape;
+
+typedef struct moe_lora_tensors {
+  const void* x;          /* bf16 [T, D] */
+  const void* w;          /* bf16 [N, D] */
+  const void* lora_a;     /* bf16 [L, r, D] */
+  const void* lora_b;     /* bf16 [L, N, r] */
+  const int32_t* adapter; /* int32 [T] */
+  const float* scale;     /* fp32 [L] or NULL */
+} moe_lora_tensors;
+
+int moe_lora_workspace_size(const moe_lora_shape* shape, size_t* bytes);
+int moe_lora_forward(const moe_lora_shape* shape, const moe_lora_tensors* t, void* y, float* xa,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Backward pass of moe_lora_forward for the gradients of sum_t <dy[t], y[t]>
+ * (W is frozen; `scale` gets no gradient):
+ *   u[t] = scale[a] B[a]^T dy[t]           dx[t] = W^T dy[t] + A[a]^T u[t]
+ *   da[l] = sum over rows of l of u[t] x[t]^T
+ *   db[l] = scale[l] * sum over rows of l of dy[t] xa[t]^T
+ *   dy  bf16 [T, N];  xa fp32 [T, r] as the forward wrote it
+ *   dx  [T, D] (out_dtype), da fp32 [L, r, D], db fp32 [L, N, r], all overwritten;
+ *       adapters no row names get zeros (also for T == 0)
+ * Limits as the forward's, and L <= 256.  u and xa enter their products as two
+ * bf16 parts.  Fixed summation order: bitwise reproducible.
+ */
+typedef struct moe_lora_grads {
+  void* dx;  /* [T, D] */
+  float* da; /* [L, r, D] */
+  float* db; /* [L, N, r] */
+} moe_lora_grads;
+
+int moe_lora_backward_workspace_size(const moe_lora_shape* shape, size_t* bytes);
+int moe_lora_backward(const moe_lora_shape* shape, const moe_lora_tensors* t, const void* dy,
+                      const float* xa, const moe_lora_grads* grads, void* workspace,
+                      size_t ws_bytes, void* stream);
+
+/*
+ * Orthogonalised updates of stacked matrices (the expert weight gradients of
+ * moe_backward or moe_grouped_gemm_wgrad, as they are): for each of the E matrices
+ * G [M, N], X = G / (|G|_F + eps), then `steps` times
+ *   X <- a X + (b P + c P P) X,   P = X X^T,   (a, b, c) = (3.4445, -4.7750, 2.0315)
+ * (for M > N the same from the other side, P = X^T X), which carries every
+ * singular value that is not far below the largest to about 1.
+ *   g    [E, M, N], fp32 or bf16 (g_dtype)
+ *   out  bf16 [E, M, N]; a matrix of zeros gives zeros
+ * Operands of the products are fp16 with power-of-two scales, sums fp32; X itself is
+ * carried between the steps in two fp16 parts (22 bits).
+ * Limits: 0 <= E <= 256, M and N multiples of 8 in [8, 32768], M * N * 4 < 2^31,
+ * min(M, N)^2 * 4 < 2^31, 1 <= steps <= 16, eps >= 0 and finite.  E == 0 does nothing.
+ */
+int moe_orthogonalize_workspace_size(int32_t E, int32_t M, int32_t N, size_t* bytes);
+int moe_orthogonalize(int32_t E, int32_t M, int32_t N, const void* g, int32_t g_dtype,
+                      int32_t steps, float eps, void* out, void* workspace, size_t ws_bytes,
+                      void* stream);
+
 /* Static text for an error code (for MOE_ERR_HIP: the last HIP error seen by
  * this thread).  Never NULL. */
 const char* moe_strerror(int code);

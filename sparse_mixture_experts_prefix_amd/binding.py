@@ -28,7 +28,10 @@ STATIC_SCRATCH_BYTES = 64 << 20  # MOE_STATIC_SCRATCH_BYTES: moe_forward_noalloc
 EXPORTS = ("moe_workspace_size", "moe_block_m", "moe_forward", "moe_route", "moe_align",
            "moe_forward_routed", "moe_forward_timed", "moe_expert_load",
            "moe_backward_workspace_size", "moe_backward", "moe_train_workspace_size",
-           "moe_forward_train", "moe_backward_saved", "moe_forward_noalloc", "moe_strerror")
+           "moe_forward_train", "moe_backward_saved", "moe_forward_noalloc",
+           "moe_grouped_gemm_workspace_size", "moe_grouped_gemm", "moe_grouped_gemm_wgrad",
+           "moe_lora_workspace_size", "moe_lora_forward", "moe_lora_backward_workspace_size",
+           "moe_lora_backward", "moe_orthogonalize_workspace_size", "moe_orthogonalize", "moe_strerror")
 
 
 class MoEError(RuntimeError):
@@ -56,6 +59,26 @@ class Grads(ctypes.Structure):
     _fields_ = [("dx", ctypes.c_void_p), ("dw_g", ctypes.c_void_p), ("d_bias", ctypes.c_void_p),
                 ("dw_gate_up", ctypes.c_void_p), ("dw_down", ctypes.c_void_p),
                 ("dws_gate_up", ctypes.c_void_p), ("dws_down", ctypes.c_void_p)]
+
+
+class GemmShape(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("G", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("weight_format", ctypes.c_int32), ("weight_layout", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
+
+
+class LoraShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("D", ctypes.c_int32), ("N", ctypes.c_int32), ("L", ctypes.c_int32),
+                ("r", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class LoraTensors(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("w", ctypes.c_void_p), ("lora_a", ctypes.c_void_p),
+                ("lora_b", ctypes.c_void_p), ("adapter", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class LoraGrads(ctypes.Structure):
+    _fields_ = [("dx", ctypes.c_void_p), ("da", ctypes.c_void_p), ("db", ctypes.c_void_p)]
 
 
 _lib = None
@@ -96,6 +119,20 @@ def load_library(path: str = LIB_PATH):
                                                ctypes.c_size_t, P]
             lib.moe_forward_noalloc.argtypes = [ctypes.POINTER(Shape), ctypes.POINTER(Weights), P, P,
                                                 P, P]
+            size_p = ctypes.POINTER(ctypes.c_size_t)
+            gemm_p, lora_p = ctypes.POINTER(GemmShape), ctypes.POINTER(LoraShape)
+            lib.moe_grouped_gemm_workspace_size.argtypes = [gemm_p, size_p]
+            lib.moe_grouped_gemm.argtypes = [gemm_p, P, P, P, P, P, P, ctypes.c_size_t, P]
+            lib.moe_grouped_gemm_wgrad.argtypes = [gemm_p, P, P, P, P, P]
+            lib.moe_lora_workspace_size.argtypes = [lora_p, size_p]
+            lib.moe_lora_forward.argtypes = [lora_p, ctypes.POINTER(LoraTensors), P, P, P,
+                                             ctypes.c_size_t, P]
+            lib.moe_lora_backward_workspace_size.argtypes = [lora_p, size_p]
+            lib.moe_lora_backward.argtypes = [lora_p, ctypes.POINTER(LoraTensors), P, P,
+                                              ctypes.POINTER(LoraGrads), P, ctypes.c_size_t, P]
+            lib.moe_orthogonalize_workspace_size.argtypes = [i32, i32, i32, size_p]
+            lib.moe_orthogonalize.argtypes = [i32, i32, i32, P, i32, i32, ctypes.c_float, P, P,
+                                              ctypes.c_size_t, P]
             lib.moe_strerror.argtypes = [ctypes.c_int]
             lib.moe_strerror.restype = ctypes.c_char_p
             for name in EXPORTS[:-1]:
@@ -496,6 +533,228 @@ moe_backward_workspace_size = backward_workspace_size
 moe_train_workspace_size = train_workspace_size
 moe_block_m = block_m
 moe_strerror = strerror
+
+
+# ------------------------------------------------- products, adapters, updates
+# moe.h's MOE_DTYPE_* and MOE_LAYOUT_* values
+DTYPE_F32 = 0
+DTYPE_BF16 = 1
+LAYOUT_NK = 0
+LAYOUT_KN = 1
+
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _dtype_code(dtype, name):
+    if dtype not in _DTYPES:
+        raise ValueError("%s must be torch.float32 or torch.bfloat16, got %s" % (name, dtype))
+    return _DTYPES[dtype]
+
+
+def _same_device(first, *rest):
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors must be on one device")
+
+
+def _sized(fn, *args) -> int:
+    n = ctypes.c_size_t(0)
+    _check(fn(*args, ctypes.byref(n)))
+    return n.value
+
+
+def _workspace(workspace, nbytes, device):
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    return _dev(workspace, "workspace", torch.uint8)
+
+
+def _gemm_shape(x, w, transposed, out_dtype) -> GemmShape:
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [R, K] and w [G, N, K] (transposed: [G, K, N])")
+    G, N, K = (w.shape[0], w.shape[2], w.shape[1]) if transposed else tuple(w.shape)
+    if x.shape[1] != K:
+        raise ValueError("x has width %d, the weights take %d" % (x.shape[1], K))
+    fmt = WEIGHTS_FP8_E4M3 if w.dtype == torch.uint8 else WEIGHTS_BF16
+    return GemmShape(x.shape[0], G, N, K, fmt, LAYOUT_KN if transposed else LAYOUT_NK, out_dtype)
+
+
+def moe_grouped_gemm_workspace_size(x, w, *, transposed=False) -> int:
+    """Workspace bytes of moe_grouped_gemm for tensors of these shapes."""
+    shape = _gemm_shape(x, w, transposed, DTYPE_F32)
+    return _sized(load_library().moe_grouped_gemm_workspace_size, ctypes.byref(shape))
+
+
+def moe_grouped_gemm(x, offsets, w, *, w_scale=None, transposed=False, out_dtype=None, y=None,
+                     workspace=None):
+    """Grouped products: y[r] = x[r] w[g]^T (transposed=True: x[r] w[g]) for the
+    rows offsets[g] <= r < offsets[g + 1].  Returns y [R, N].
+
+    x bf16 [R, K]; offsets int32 [G + 1] on the GPU; w bf16 [G, N, K]
+    (transposed: [G, K, N]) or uint8 E4M3 codes [G, N, K] with w_scale fp32
+    [G, N].  out_dtype: torch.float32 (default) or torch.bfloat16; y's own type
+    when y is given.  Rows of no group keep what y held.  The gradient of x of
+    a call with weights w is moe_grouped_gemm(dy, offsets, w, transposed=True).
+    """
+    _dev(x, "x", torch.bfloat16)
+    if w is None or w.dtype not in (torch.bfloat16, torch.uint8):
+        raise ValueError("w must be bf16 or uint8 (E4M3 codes)")
+    _dev(w, "w", w.dtype)
+    if out_dtype is None:
+        out_dtype = torch.float32 if y is None else y.dtype
+    shape = _gemm_shape(x, w, transposed, _dtype_code(out_dtype, "out_dtype"))
+    _dev(offsets, "offsets", torch.int32, (shape.G + 1,))
+    if w.dtype == torch.uint8:
+        _dev(w_scale, "w_scale", torch.float32, (shape.G, shape.N))
+    elif w_scale is not None:
+        raise ValueError("w_scale is only for uint8 (E4M3) weights")
+    lib = load_library()
+    with torch.cuda.device(x.device):
+        if y is None:
+            y = torch.empty((shape.R, shape.N), dtype=out_dtype, device=x.device)
+        _dev(y, "y", out_dtype, (shape.R, shape.N))
+        workspace = _workspace(workspace, _sized(lib.moe_grouped_gemm_workspace_size,
+                                                 ctypes.byref(shape)), x.device)
+        _same_device(x, offsets, w, w_scale, y, workspace)
+        _check(lib.moe_grouped_gemm(ctypes.byref(shape), _ptr(x), _ptr(offsets), _ptr(w), _ptr(w_scale),
+                                    _ptr(y), _ptr(workspace), workspace.numel(), _stream(x.device)))
+    return y
+
+
+def moe_grouped_gemm_wgrad(dy, x, offsets, *, dw=None):
+    """The gradient of w [G, N, K] of moe_grouped_gemm(x, offsets, w):
+    dw[g] = sum of dy[r]^T x[r] over the group's rows, fp32, zeros for groups
+    without rows.  dy bf16 [R, N], x bf16 [R, K].  Returns dw."""
+    _dev(dy, "dy", torch.bfloat16)
+    _dev(x, "x", torch.bfloat16)
+    _dev(offsets, "offsets", torch.int32)
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0] or offsets.dim() != 1:
+        raise ValueError("dy must be [R, N], x [R, K] and offsets [G + 1]")
+    shape = GemmShape(x.shape[0], offsets.shape[0] - 1, dy.shape[1], x.shape[1], WEIGHTS_BF16, LAYOUT_NK,
+                      DTYPE_F32)
+    with torch.cuda.device(x.device):
+        if dw is None:
+            dw = torch.empty((max(shape.G, 0), shape.N, shape.K), dtype=torch.float32, device=x.device)
+        _dev(dw, "dw", torch.float32, (shape.G, shape.N, shape.K))
+        _same_device(x, dy, offsets, dw)
+        _check(load_library().moe_grouped_gemm_wgrad(ctypes.byref(shape), _ptr(dy), _ptr(x), _ptr(offsets),
+                                                     _ptr(dw), _stream(x.device)))
+    return dw
+
+
+def _lora_shape(x, w, lora_a, out_dtype=DTYPE_F32) -> LoraShape:
+    if x.dim() != 2 or w.dim() != 2 or lora_a.dim() != 3:
+        raise ValueError("x must be [T, D], w [N, D] and lora_a [L, r, D]")
+    return LoraShape(x.shape[0], x.shape[1], w.shape[0], lora_a.shape[0], lora_a.shape[1], out_dtype)
+
+
+def moe_lora_workspace_size(x, w, lora_a) -> int:
+    """Workspace bytes of moe_lora_forward for tensors of these shapes."""
+    return _sized(load_library().moe_lora_workspace_size, ctypes.byref(_lora_shape(x, w, lora_a)))
+
+
+def moe_lora_backward_workspace_size(x, w, lora_a) -> int:
+    """Workspace bytes of moe_lora_backward for tensors of these shapes."""
+    return _sized(load_library().moe_lora_backward_workspace_size, ctypes.byref(_lora_shape(x, w, lora_a)))
+
+
+def _check_lora(x, w, lora_a, lora_b, adapter, scale, out_dtype):
+    _dev(x, "x", torch.bfloat16)
+    _dev(w, "w", torch.bfloat16)
+    _dev(lora_a, "lora_a", torch.bfloat16)
+    shape = _lora_shape(x, w, lora_a, _dtype_code(out_dtype, "the output's type"))
+    if w.shape[1] != shape.D or lora_a.shape[2] != shape.D:
+        raise ValueError("x, w and lora_a must share their last dimension")
+    _dev(lora_b, "lora_b", torch.bfloat16, (shape.L, shape.N, shape.r))
+    _dev(adapter, "adapter", torch.int32, (shape.T,))
+    if scale is not None:
+        _dev(scale, "scale", torch.float32, (shape.L,))
+    _same_device(x, w, lora_a, lora_b, adapter, scale)
+    return shape, LoraTensors(_ptr(x), _ptr(w), _ptr(lora_a), _ptr(lora_b), _ptr(adapter), _ptr(scale))
+
+
+def moe_lora_forward(x, w, lora_a, lora_b, adapter, scale=None, *, out_dtype=None, y=None, xa=None,
+                     workspace=None):
+    """y[t] = W x[t] + scale[a] B[a] (A[a] x[t]) with a = adapter[t]; rows whose
+    adapter is negative or past the last get W x[t].  Returns y [T, N].
+
+    x bf16 [T, D]; w bf16 [N, D]; lora_a bf16 [L, r, D]; lora_b bf16 [L, N, r];
+    adapter int32 [T]; scale fp32 [L] or None (1).  out_dtype: torch.bfloat16
+    (default) or torch.float32; y's own type when y is given.  xa (fp32 [T, r]):
+    filled with A[a] x[t], which moe_lora_backward takes.
+    """
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if y is None else y.dtype
+    shape, t = _check_lora(x, w, lora_a, lora_b, adapter, scale, out_dtype)
+    lib = load_library()
+    with torch.cuda.device(x.device):
+        if y is None:
+            y = torch.empty((shape.T, shape.N), dtype=out_dtype, device=x.device)
+        _dev(y, "y", out_dtype, (shape.T, shape.N))
+        if xa is not None:
+            _dev(xa, "xa", torch.float32, (shape.T, shape.r))
+        workspace = _workspace(workspace, _sized(lib.moe_lora_workspace_size, ctypes.byref(shape)), x.device)
+        _same_device(x, y, xa, workspace)
+        _check(lib.moe_lora_forward(ctypes.byref(shape), ctypes.byref(t), _ptr(y), _ptr(xa),
+                                    _ptr(workspace), workspace.numel(), _stream(x.device)))
+    return y
+
+
+def moe_lora_backward(x, w, lora_a, lora_b, adapter, dy, xa, scale=None, *, out_dtype=None, grads=None,
+                      workspace=None):
+    """Gradients of sum <dy, y> of a moe_lora_forward call (W is frozen).
+    Returns a dict: dx [T, D] (out_dtype, fp32 by default), da fp32 [L, r, D],
+    db fp32 [L, N, r]; ``grads`` may hold preallocated ones.  dy bf16 [T, N]; xa
+    fp32 [T, r] as the forward filled it.  At most 256 adapters."""
+    out = dict(grads or {})
+    if out_dtype is None:
+        out_dtype = out["dx"].dtype if "dx" in out else torch.float32
+    shape, t = _check_lora(x, w, lora_a, lora_b, adapter, scale, out_dtype)
+    _dev(dy, "dy", torch.bfloat16, (shape.T, shape.N))
+    _dev(xa, "xa", torch.float32, (shape.T, shape.r))
+    lib = load_library()
+    with torch.cuda.device(x.device):
+        for name, dtype, size in (("dx", out_dtype, (shape.T, shape.D)),
+                                  ("da", torch.float32, (shape.L, shape.r, shape.D)),
+                                  ("db", torch.float32, (shape.L, shape.N, shape.r))):
+            if name not in out:
+                out[name] = torch.empty(size, dtype=dtype, device=x.device)
+            _dev(out[name], name, dtype, size)
+        workspace = _workspace(workspace, _sized(lib.moe_lora_backward_workspace_size, ctypes.byref(shape)),
+                               x.device)
+        _same_device(x, dy, xa, out["dx"], out["da"], out["db"], workspace)
+        g = LoraGrads(_ptr(out["dx"]), _ptr(out["da"]), _ptr(out["db"]))
+        _check(lib.moe_lora_backward(ctypes.byref(shape), ctypes.byref(t), _ptr(dy), _ptr(xa),
+                                     ctypes.byref(g), _ptr(workspace), workspace.numel(),
+                                     _stream(x.device)))
+    return out
+
+
+def moe_orthogonalize_workspace_size(g) -> int:
+    """Workspace bytes of moe_orthogonalize for a stack [E, M, N] of this shape."""
+    if g.dim() != 3:
+        raise ValueError("g must be [E, M, N]")
+    return _sized(load_library().moe_orthogonalize_workspace_size, *g.shape)
+
+
+def moe_orthogonalize(g, *, steps=5, eps=1e-7, out=None, workspace=None):
+    """The orthogonalised update of every matrix of g [E, M, N] (fp32 or bf16)
+    by `steps` Newton-Schulz steps (see moe_orthogonalize in moe.h).  Returns
+    out, bf16 [E, M, N]."""
+    if g is None or g.dtype not in _DTYPES:
+        raise ValueError("g must be fp32 or bf16")
+    _dev(g, "g", g.dtype)
+    nbytes = moe_orthogonalize_workspace_size(g)
+    with torch.cuda.device(g.device):
+        if out is None:
+            out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+        _dev(out, "out", torch.bfloat16, tuple(g.shape))
+        workspace = _workspace(workspace, nbytes, g.device)
+        _same_device(g, out, workspace)
+        _check(load_library().moe_orthogonalize(*g.shape, _ptr(g), _DTYPES[g.dtype], int(steps), float(eps),
+                                                _ptr(out), _ptr(workspace), workspace.numel(),
+                                                _stream(g.device)))
+    return out
 
 
 # ------------------------------------------------------------------ timing

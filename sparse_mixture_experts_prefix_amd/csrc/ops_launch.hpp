@@ -1,0 +1,25 @@
+// Launchers of the grouped products, the adapters and the orthogonalised
+// update (host functions defined next to their kernels).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ops_plan.hpp"
+
+namespace moe {
+
+hipError_t launch_grouped_gemm(const moe_gemm_shape& s, const GemmPlan& p, const void* x,
+                               const int32_t* offsets, const void* w, const float* w_scale, void* y,
+                               void* ws, hipStream_t st);
+hipError_t launch_grouped_wgrad(const moe_gemm_shape& s, const void* dy, const void* x,
+                                const int32_t* offsets, float* dw, hipStream_t st);
+hipError_t launch_lora_forward(const moe_lora_shape& s, const LoraPlan& p, const moe_lora_tensors& t,
+                               void* y, float* xa, void* ws, hipStream_t st);
+hipError_t launch_lora_backward(const moe_lora_shape& s, const LoraBwdPlan& p,
+                                const moe_lora_tensors& t, const void* dy, const float* xa,
+                                const moe_lora_grads& g, void* ws, hipStream_t st);
+hipError_t launch_orthogonalize(int E, int M, int N, const OrthPlan& p, const void* g, int g_dtype,
+                                int steps, float eps, void* out, void* ws, hipStream_t st);
+
+
+}  // namespace moe

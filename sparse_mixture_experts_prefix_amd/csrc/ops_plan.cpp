@@ -1,0 +1,125 @@
+// Host-side argument checks and workspace layout (no HIP calls).
+#include "ops_plan.hpp"
+
+#include "plan.hpp"
+
+namespace moe {
+
+namespace {
+constexpr int64_t kLim31 = int64_t(1) << 31;
+constexpr int64_t kMaxTiles = int64_t(1) << 23;  // workgroups of a launch (256 threads each)
+
+struct Layout {
+  size_t o = 0;
+  size_t take(size_t bytes) {
+    const size_t at = o;
+    o += (bytes + 255) / 256 * 256;
+    return at;
+  }
+};
+
+// a tile's rows (up to 288 of them) are addressed with 32-bit byte offsets
+bool width_ok(int64_t w) { return 288 * 4 * w < kLim31; }
+bool mult8(int64_t v) { return v > 0 && v % 8 == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+}  // namespace
+
+int check_gemm_shape(const moe_gemm_shape* s) {
+  if (!s) return MOE_ERR_INVALID_ARG;
+  if (s->R < 0 || s->G <= 0 || !mult8(s->N) || !mult8(s->K)) return MOE_ERR_INVALID_ARG;
+  if (s->weight_format != MOE_WEIGHTS_BF16 && s->weight_format != MOE_WEIGHTS_FP8_E4M3)
+    return MOE_ERR_INVALID_ARG;
+  if (s->weight_layout != MOE_LAYOUT_NK && s->weight_layout != MOE_LAYOUT_KN)
+    return MOE_ERR_INVALID_ARG;
+  if (s->out_dtype != MOE_DTYPE_F32 && s->out_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (s->G > 256) return MOE_ERR_UNSUPPORTED;
+  // E4M3 scales belong to rows of w, which the transposed product sums over
+  if (s->weight_format == MOE_WEIGHTS_FP8_E4M3 && s->weight_layout == MOE_LAYOUT_KN)
+    return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)s->N * s->K * 2 >= kLim31 || !width_ok(s->N) || !width_ok(s->K))
+    return MOE_ERR_UNSUPPORTED;
+  // row indices, and the workgroups of the smallest tiles of 256 x 64
+  if ((int64_t)s->R + 256 * 257 >= kLim31) return MOE_ERR_UNSUPPORTED;
+  if (((int64_t)s->R / 256 + 2 * s->G) * (s->N / 64 + 1) >= kMaxTiles) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int check_gemm_wgrad_shape(const moe_gemm_shape* s) {
+  const int rc = check_gemm_shape(s);
+  if (rc) return rc;
+  if (s->weight_format || s->weight_layout || s->out_dtype) return MOE_ERR_INVALID_ARG;
+  const int64_t w = s->N > s->K ? s->N : s->K;
+  if ((int64_t)s->R * w * 2 >= kLim31 || (int64_t)s->N * s->K * 4 >= kLim31)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int make_gemm_plan(const moe_gemm_shape* s, GemmPlan* p) {
+  const int rc = check_gemm_shape(s);
+  if (rc) return rc;
+  p->total = 0;
+  return MOE_OK;
+}
+
+int check_lora_shape(const moe_lora_shape* s) {
+  if (!s) return MOE_ERR_INVALID_ARG;
+  if (s->T < 0 || s->L <= 0 || !mult8(s->D) || !mult8(s->N) || !mult8(s->r))
+    return MOE_ERR_INVALID_ARG;
+  if (s->out_dtype != MOE_DTYPE_F32 && s->out_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (s->L > kLoraMaxAdapters || s->r > kLoraMaxRank) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)s->N * s->D * 2 >= kLim31 || !width_ok(s->N) || !width_ok(s->D))
+    return MOE_ERR_UNSUPPORTED;
+  const int64_t w = s->N > s->D ? s->N : s->D;
+  if (((int64_t)s->T / 256 + 1) * (w / 64 + 1) >= kMaxTiles || s->T > kLoraMaxRows)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int check_lora_tensors(const moe_lora_shape* s, const moe_lora_tensors* t) {
+  if (!t || !t->w || !t->lora_a || !t->lora_b) return MOE_ERR_INVALID_ARG;
+  if (s->T > 0 && (!t->x || !t->adapter)) return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {t->x, t->w, t->lora_a, t->lora_b};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return MOE_ERR_ALIGNMENT;
+  if (!aligned4(t->adapter) || !aligned4(t->scale)) return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+
+int make_lora_plan(const moe_lora_shape* s, LoraPlan* p) {
+  const int rc = check_lora_shape(s);
+  if (rc) return rc;
+  Layout l;
+  p->off_xa = l.take(sizeof(float) * (size_t)s->T * s->r);
+  p->total = l.o;
+  return MOE_OK;
+}
+
+int make_lora_backward_plan(const moe_lora_shape* s, LoraBwdPlan* p) {
+  const int rc = check_lora_shape(s);
+  if (rc) return rc;
+  if (s->L > kLoraMaxTrained) return MOE_ERR_UNSUPPORTED;
+  Layout l;
+  p->off_u = l.take(sizeof(float) * (size_t)s->T * s->r);
+  p->total = l.o;
+  return MOE_OK;
+}
+
+int make_orth_plan(int32_t E, int32_t M, int32_t N, OrthPlan* p) {
+  if (E < 0 || !mult8(M) || !mult8(N)) return MOE_ERR_INVALID_ARG;
+  if (E > 256 || M > 32768 || N > 32768) return MOE_ERR_UNSUPPORTED;
+  p->m = M < N ? M : N;
+  p->n = M < N ? N : M;
+  p->tall = M > N;
+  if ((int64_t)M * N * 4 >= kLim31 || (int64_t)p->m * p->m * 4 >= kLim31) return MOE_ERR_UNSUPPORTED;
+  Layout l;
+  const size_t mn = sizeof(float) * (size_t)E * M * N, mm = sizeof(float) * (size_t)E * p->m * p->m;
+  p->off_x[0] = l.take(mn);
+  p->off_x[1] = l.take(mn);
+  p->off_p = l.take(mm);
+  p->off_q = l.take(mm);
+  p->off_norm = l.take(sizeof(float) * E);
+  p->total = l.o;
+  return MOE_OK;
+}
+
+}  // namespace moe

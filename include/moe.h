@@ -374,7 +374,7 @@ int moe_backward_saved(const moe_shape* shape, const moe_weights* w, const int32
  *   workspace  device buffer of ws_bytes >= moe_grouped_gemm_workspace_size(shape)
  *            (NULL when that is 0)
  * Limits: 0 <= R, 1 <= G <= 256, N and K positive multiples of 8, N * K * 2 < 2^31,
- * 288 * 4 * max(N, K) < 2^31, R + 256 * 257 < 2^31, (R / 256 + 2 G) (N / 64 + 1) < 2^23.
+ * 288 * 4 * max(N, K) < 2^31, R + 256 * 257 < 2^31, (R / 32 + 2 G) (N / 64 + 1) < 2^23.
  * R == 0 does nothing.  Products of bf16 values are exact, sums fp32 in a
  * fixed order: the same call gives bitwise the same rows.
  */

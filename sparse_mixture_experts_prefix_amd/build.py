@@ -15,8 +15,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["router.hip", "align.hip", "gemm_prefill.hip", "gemm_decode.hip", "combine.hip",
-           "backward.hip", "scratch.hip", "grouped.hip", "lora.hip", "orthogonalize.hip", "api.cpp",
-           "plan.cpp", "ops_api.cpp", "ops_plan.cpp"]
+           "backward.hip", "scratch.hip", "grouped.hip", "grouped_prefill.hip",
+           "grouped_wgrad.hip", "lora.hip", "orthogonalize.hip", "api.cpp", "plan.cpp", "ops_api.cpp", "ops_plan.cpp"]
 
 CFLAGS = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,

@@ -28,10 +28,12 @@ T* at(void* base, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(base) + off);
 }
 
+}  // namespace
+
 // Compute units of the current device, capped at the split workspace size:
 // the prefill GEMMs balance their last round of tiles over this many
 // workgroups (one resident per CU).
-hipError_t split_ctas(int* out) {
+hipError_t moe::split_ctas(int* out) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
@@ -48,6 +50,10 @@ hipError_t split_ctas(int* out) {
   *out = n;
   return hipSuccess;
 }
+
+namespace {
+
+using moe::split_ctas;
 
 // Records events[i] on the stream when timing is requested.
 struct Marks {

@@ -11,6 +11,10 @@ namespace moe {
 // thread and returns MOE_ERR_HIP.
 int record_hip_error(hipError_t e);
 
+// Workgroups of 256 x 256 tiles that run at once on the current device (one
+// per CU, at most kSplitCtas).
+hipError_t split_ctas(int* out);
+
 // moe_forward's host checks of every argument but the workspace: an error
 // code, or MOE_OK (also for T == 0, where the call does nothing).
 int check_forward_args(const moe_shape* shape, const moe_weights* w, const float* y,
@@ -42,6 +46,8 @@ hipError_t launch_align(const int32_t* ids, int T, int k, int E, int id_base, in
 hipError_t launch_fill_i32(int32_t* out, int64_t n, int32_t v, hipStream_t s);
 
 struct GroupedGemm {
+  static constexpr bool kRagged = false;  // groups are padded to BM rows
+  static constexpr bool kFold = true;     // short last m-tiles fold into the one before
   const uint16_t* A;          // gate/up: x [T, D] (rows gathered by row_token); down: H
   const int32_t* row_token;   // gate/up only
   int64_t lda;                // elements

@@ -5,12 +5,15 @@
 #include <stdint.h>
 
 #include "ops_plan.hpp"
+#include "ragged.hpp"
 
 namespace moe {
 
 hipError_t launch_grouped_gemm(const moe_gemm_shape& s, const GemmPlan& p, const void* x,
                                const int32_t* offsets, const void* w, const float* w_scale, void* y,
                                void* ws, hipStream_t st);
+// groups of many rows: mtiles bounds the 256-row tiles that hold rows
+hipError_t launch_grouped_prefill(RaggedGemm p, bool fp8, bool kn, int64_t mtiles, hipStream_t s);
 hipError_t launch_grouped_wgrad(const moe_gemm_shape& s, const void* dy, const void* x,
                                 const int32_t* offsets, float* dw, hipStream_t st);
 hipError_t launch_lora_forward(const moe_lora_shape& s, const LoraPlan& p, const moe_lora_tensors& t,

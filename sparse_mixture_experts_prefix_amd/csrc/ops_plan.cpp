@@ -20,6 +20,13 @@ struct Layout {
 
 // a tile's rows (up to 288 of them) are addressed with 32-bit byte offsets
 bool width_ok(int64_t w) { return 288 * 4 * w < kLim31; }
+// Whether the 256-row tile kernels may cut their last round along K: K long
+// enough for two pieces of four 64-wide stages, and fewer than four rounds of
+// tiles on the largest chip (see split_of in gemm_tile.hpp).
+constexpr size_t kPartialBytes = sizeof(float) * kSplitCtas * kPartialTileFloats;
+bool may_split(int64_t mtiles, int64_t N, int64_t K) {
+  return (K + 63) / 64 >= 8 && mtiles * ((N + 255) / 256) < 4 * kSplitCtas;
+}
 bool mult8(int64_t v) { return v > 0 && v % 8 == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 }  // namespace
@@ -38,9 +45,9 @@ int check_gemm_shape(const moe_gemm_shape* s) {
     return MOE_ERR_UNSUPPORTED;
   if ((int64_t)s->N * s->K * 2 >= kLim31 || !width_ok(s->N) || !width_ok(s->K))
     return MOE_ERR_UNSUPPORTED;
-  // row indices, and the workgroups of the smallest tiles of 256 x 64
+  // row indices, and the workgroups of the smallest tiles of 32 x 64
   if ((int64_t)s->R + 256 * 257 >= kLim31) return MOE_ERR_UNSUPPORTED;
-  if (((int64_t)s->R / 256 + 2 * s->G) * (s->N / 64 + 1) >= kMaxTiles) return MOE_ERR_UNSUPPORTED;
+  if (((int64_t)s->R / 32 + 2 * s->G) * (s->N / 64 + 1) >= kMaxTiles) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -57,7 +64,13 @@ int check_gemm_wgrad_shape(const moe_gemm_shape* s) {
 int make_gemm_plan(const moe_gemm_shape* s, GemmPlan* p) {
   const int rc = check_gemm_shape(s);
   if (rc) return rc;
-  p->total = 0;
+  // tile rows by mean rows per group, as the layer's (choose_block_m): few rows
+  // stream the weights.  E4M3 codes move in 16-code chunks in the 256-row tiles.
+  const int64_t rows = s->R;
+  p->BM = rows <= (int64_t)20 * s->G ? 16 : rows <= (int64_t)48 * s->G ? 32 : 256;
+  if (p->BM == 256 && s->weight_format == MOE_WEIGHTS_FP8_E4M3 && s->K % 16) p->BM = 32;
+  p->split = p->BM == 256 && may_split((rows + 255) / 256, s->N, s->K);
+  p->total = p->split ? kPartialBytes : 0;
   return MOE_OK;
 }
 

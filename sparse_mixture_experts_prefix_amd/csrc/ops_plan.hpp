@@ -14,7 +14,9 @@ int check_gemm_shape(const moe_gemm_shape* s);
 int check_gemm_wgrad_shape(const moe_gemm_shape* s);
 
 struct GemmPlan {
-  size_t total;  // workspace bytes
+  int BM;        // rows per tile: 16 and 32 stream the weights, 256 are MFMA-bound
+  int split;     // the last round of 256-row tiles may be cut along K
+  size_t total;  // workspace bytes (fp32 partial tiles of the cut)
 };
 int make_gemm_plan(const moe_gemm_shape* s, GemmPlan* p);
 

@@ -456,7 +456,7 @@ int moe_lora_forward(const moe_lora_shape* shape, const moe_lora_tensors* t, voi
  *   dy  bf16 [T, N];  xa fp32 [T, r] as the forward wrote it
  *   dx  [T, D] (out_dtype), da fp32 [L, r, D], db fp32 [L, N, r], all overwritten;
  *       adapters no row names get zeros (also for T == 0)
- * Limits as the forward's, and L <= 256.  u and xa enter their products as two
+ * Limits as the forward's, and L <= 256, T * max(N, D) * 2 < 2^31, T * r * 4 < 2^31.  u and xa enter their products as two
  * bf16 parts.  Fixed summation order: bitwise reproducible.
  */
 typedef struct moe_lora_grads {

@@ -16,7 +16,8 @@ ARCH = "gfx950"
 
 SOURCES = ["router.hip", "align.hip", "gemm_prefill.hip", "gemm_decode.hip", "combine.hip",
            "backward.hip", "scratch.hip", "grouped.hip", "grouped_prefill.hip",
-           "grouped_wgrad.hip", "lora.hip", "orthogonalize.hip", "api.cpp", "plan.cpp", "ops_api.cpp", "ops_plan.cpp"]
+           "grouped_wgrad.hip", "lora.hip", "lora_prefill.hip", "lora_decode.hip", "lora_wgrad.hip",
+           "orthogonalize.hip", "api.cpp", "plan.cpp", "ops_api.cpp", "ops_plan.cpp"]
 
 CFLAGS = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,

@@ -33,6 +33,10 @@ __device__ __forceinline__ bf16_t f32_to_bf16(float f) {
   return __builtin_bit_cast(bf16_t, (__bf16)f);  // round to nearest even
 }
 
+__device__ __forceinline__ float bf16_to_f32(bf16_t v) {
+  return __builtin_bit_cast(float, (uint32_t)v << 16);
+}
+
 // SiLU(g) = g / (1 + e^-g) with the hardware exp2 and reciprocal (each about
 // 1 ulp in fp32); the result is rounded to bf16 right after, 2^16 times coarser.
 __device__ __forceinline__ float silu(float g) {

@@ -763,6 +763,11 @@ __device__ __forceinline__ void prefill_tile(const P& p, char* lds) {
   // carry them, so their registers and schedule stay as they were.
   auto finish = [&](auto xrt, ExtraRows* xr) {
     constexpr bool XRT = decltype(xrt)::value;
+    // adapters: their second product, once per tile (in the last piece of a cut one)
+    if constexpr (P::kLora) {
+      if (!piece || part == S - 1)
+        lora_expand<KMAJ>(p, lds, row0, valid_rows, n0, wm, wn, il, acc);
+    }
     // E4M3: every output column times the scale of its weight row
     if constexpr (FP8) {
       const float* Sg = shared ? p.S_shared : p.S_routed + (int64_t)g * brows;

@@ -48,6 +48,8 @@ hipError_t launch_fill_i32(int32_t* out, int64_t n, int32_t v, hipStream_t s);
 struct GroupedGemm {
   static constexpr bool kRagged = false;  // groups are padded to BM rows
   static constexpr bool kFold = true;     // short last m-tiles fold into the one before
+  static constexpr bool kLora = false;    // no adapters beside the product
+  static constexpr bool kParts = false;   // few-row tiles: a workgroup takes all of K
   const uint16_t* A;          // gate/up: x [T, D] (rows gathered by row_token); down: H
   const int32_t* row_token;   // gate/up only
   int64_t lda;                // elements

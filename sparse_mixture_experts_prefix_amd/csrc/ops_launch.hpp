@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "lora.hpp"
 #include "ops_plan.hpp"
 #include "ragged.hpp"
 
@@ -21,6 +22,21 @@ hipError_t launch_lora_forward(const moe_lora_shape& s, const LoraPlan& p, const
 hipError_t launch_lora_backward(const moe_lora_shape& s, const LoraBwdPlan& p,
                                 const moe_lora_tensors& t, const void* dy, const float* xa,
                                 const moe_lora_grads& g, void* ws, hipStream_t st);
+// out = in w^T + the adapters' second product (kmajor: w and the adapters as the
+// backward pass reads them).  Many rows: parts16 holds the first product's two
+// bf16 parts; partial (or NULL: no cut along K) room for partial tiles.
+hipError_t launch_lora_prefill(const LoraCall& c, bool kmajor, const uint16_t* parts16, float* partial,
+                               hipStream_t s);
+// At most 64 rows, both products: v (or NULL), sv and parts16 (or NULL) as
+// ShrinkOut; partial [parts][T][N].
+hipError_t launch_lora_decode(const LoraCall& c, bool kmajor, float* v, float* sv, uint16_t* parts16,
+                              float* partial, int parts, hipStream_t s);
+struct LoraRows {
+  const int32_t *counts, *offsets, *sorted;  // rows by adapter (align's outputs)
+};
+hipError_t launch_lora_wgrad(const LoraRows& rows, const void* x, const void* dy, const uint16_t* u,
+                             const uint16_t* xa, const float* scale, int T, int D, int N, int L, int r,
+                             float* da, float* db, hipStream_t s);
 hipError_t launch_orthogonalize(int E, int M, int N, const OrthPlan& p, const void* g, int g_dtype,
                                 int steps, float eps, void* out, void* ws, hipStream_t st);
 

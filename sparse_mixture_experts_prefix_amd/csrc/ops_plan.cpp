@@ -98,11 +98,28 @@ int check_lora_tensors(const moe_lora_shape* s, const moe_lora_tensors* t) {
   return MOE_OK;
 }
 
+namespace {
+// Parts of K of the few-row path: about 512 workgroups of 64 columns, each
+// wave with two or more of the 64-wide K chunks.
+int few_row_parts(int64_t N, int64_t K) {
+  const int64_t tiles = (N + 63) / 64, chunks = (K + 63) / 64;
+  int64_t parts = (512 + tiles - 1) / tiles;
+  if (parts > chunks / 8) parts = chunks / 8;
+  return parts < 1 ? 1 : (int)parts;
+}
+}  // namespace
+
 int make_lora_plan(const moe_lora_shape* s, LoraPlan* p) {
   const int rc = check_lora_shape(s);
   if (rc) return rc;
+  const size_t T = s->T, r = s->r;
+  const bool few = s->T <= kLoraFewRows;
+  p->parts = few ? few_row_parts(s->N, s->D) : 0;
+  p->split = !few && may_split((s->T + 255) / 256, s->N, s->D);
   Layout l;
-  p->off_xa = l.take(sizeof(float) * (size_t)s->T * s->r);
+  p->off_sv = l.take(few ? sizeof(float) * T * r : 0);
+  p->off_v16 = l.take(few ? 0 : sizeof(uint16_t) * T * 2 * r);
+  p->off_partial = l.take(few ? sizeof(float) * p->parts * T * s->N : p->split ? kPartialBytes : 0);
   p->total = l.o;
   return MOE_OK;
 }
@@ -111,8 +128,19 @@ int make_lora_backward_plan(const moe_lora_shape* s, LoraBwdPlan* p) {
   const int rc = check_lora_shape(s);
   if (rc) return rc;
   if (s->L > kLoraMaxTrained) return MOE_ERR_UNSUPPORTED;
+  // gathered rows are addressed with 32-bit byte offsets
+  const int64_t w = s->N > s->D ? s->N : s->D;
+  if (s->T * w * 2 >= kLim31 || (int64_t)s->T * s->r * 4 >= kLim31) return MOE_ERR_UNSUPPORTED;
+  const size_t T = s->T, r = s->r;
+  const bool few = s->T <= kLoraFewRows;
+  p->parts = few ? few_row_parts(s->D, s->N) : 0;
+  p->split = !few && may_split((s->T + 255) / 256, s->D, s->N);
   Layout l;
-  p->off_u = l.take(sizeof(float) * (size_t)s->T * s->r);
+  p->off_su = l.take(few ? sizeof(float) * T * r : 0);
+  p->off_u16 = l.take(sizeof(uint16_t) * T * 2 * r);
+  p->off_xa16 = l.take(sizeof(uint16_t) * T * 2 * r);
+  p->off_rows = l.take(sizeof(int32_t) * (772 + 4 * T + 1));
+  p->off_partial = l.take(few ? sizeof(float) * p->parts * T * s->D : p->split ? kPartialBytes : 0);
   p->total = l.o;
   return MOE_OK;
 }

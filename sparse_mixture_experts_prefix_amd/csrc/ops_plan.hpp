@@ -27,14 +27,26 @@ constexpr int kLoraMaxTrained = 256;  // adapters of a backward pass (it groups 
 int check_lora_shape(const moe_lora_shape* s);
 int check_lora_tensors(const moe_lora_shape* s, const moe_lora_tensors* t);
 
+// Rows of the few-row path, which streams W with all rows in one tile.
+constexpr int kLoraFewRows = 64;
+
 struct LoraPlan {
-  size_t off_xa;     // forward: fp32 [T][r]: A x, when the caller keeps none
+  int parts;           // few rows: parts K is cut into (0: the 256-row tiles)
+  int split;           // 256-row tiles: the last round may be cut along K
+  size_t off_sv;       // few rows: fp32 [T][r], scale A x
+  size_t off_v16;      // many rows: bf16 [T][2 r], its two parts
+  size_t off_partial;  // fp32 [parts][T][N], or partial tiles
   size_t total;
 };
 int make_lora_plan(const moe_lora_shape* s, LoraPlan* p);
 
 struct LoraBwdPlan {
-  size_t off_u;      // fp32 [T][r]: scale B^T dy
+  int parts, split;    // as above, for dx
+  size_t off_su;       // few rows: fp32 [T][r], u
+  size_t off_u16;      // bf16 [T][2 r]: u's two parts
+  size_t off_xa16;     // bf16 [T][2 r]: xa's
+  size_t off_rows;     // int32 [772 + 4 T + 1]: rows by adapter (see launch_lora_backward)
+  size_t off_partial;  // fp32 [parts][T][D], or partial tiles
   size_t total;
 };
 int make_lora_backward_plan(const moe_lora_shape* s, LoraBwdPlan* p);

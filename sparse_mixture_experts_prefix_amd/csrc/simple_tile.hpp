@@ -6,10 +6,6 @@
 
 namespace moe {
 
-__device__ __forceinline__ float bf16_to_f32(bf16_t v) {
-  return __builtin_bit_cast(float, (uint32_t)v << 16);
-}
-
 // a(m, k) for m < M, b(n, k) for n < N, k < K; store(m, n, sum) for the tile at (m0, n0)
 template <class FA, class FB, class FC>
 __device__ __forceinline__ void simple_tile(FA a, FB b, FC store, int64_t M, int64_t N, int64_t K,

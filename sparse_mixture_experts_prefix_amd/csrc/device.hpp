@@ -7,6 +7,7 @@ namespace moe {
 
 typedef uint16_t bf16_t;  // raw bfloat16 storage
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -18,8 +19,14 @@ __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast
 // D(32x32, fp32) += A(32x16, bf16) * B(16x32, bf16).  Lane l supplies row l%32
 // of A and column l%32 of B, eight consecutive k each (k block l/32).  The
 // result: register r of lane l is row 8*(r/4) + 4*(l/32) + r%4, column l%32.
+// F16: the sixteen-bit operands are fp16.
+template <bool F16 = false>
 __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
 // D(16x16, fp32) += A(16x32) * B(32x16).  Lane l supplies row l%16 of A and

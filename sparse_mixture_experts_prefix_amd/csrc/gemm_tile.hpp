@@ -88,7 +88,7 @@ __device__ __forceinline__ int b_row_of(int wn, int j) {
 // the first 64 tier rows).
 // E4M3 B: four loads per wave and stage instead of eight, so B(i+3) takes
 // two per substep and the barrier waits with vmcnt(4).
-// KMAJ: B is K-major (see kmaj_chunk); KA: A is too.
+// KMAJ: B is K-major (see kmaj_chunk); KA: A is too.  F16: operands are fp16.
 // XR: the tile also computes its folded rows (see tile_rows).  Their A
 // fragments come from memory straight into registers, one 16-byte load per
 // lane and k-substep (every wave loads the same 32 rows), issued a stage
@@ -130,7 +130,7 @@ __device__ __forceinline__ void xr_settle(f32x16& c0, f32x16& c1) {
 }
 
 template <bool GATE_UP, int ACT, bool FP8, class IssueA, class IssueB, bool KMAJ = false,
-          bool KA = false, bool PRE = false, int NA = 8, bool XR = false, int XW = 0>
+          bool KA = false, bool PRE = false, int NA = 8, bool XR = false, int XW = 0, bool F16 = false>
 __device__ __forceinline__ void k_loop(const char* lds, int s0, int n, int wm, int wn, bool il,
                                        int lane, IssueA& issue_a, IssueB& issue_b,
                                        f32x16 (&acc)[4][4], ExtraRows* xr = nullptr) {
@@ -215,7 +215,7 @@ __device__ __forceinline__ void k_loop(const char* lds, int s0, int n, int wm, i
 #pragma unroll
     for (int i = 0; i < ACT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = mfma32(fa[slot][i], fb[slot][j], acc[i][j]);
+      for (int j = 0; j < 4; ++j) acc[i][j] = mfma32<F16>(fa[slot][i], fb[slot][j], acc[i][j]);
   };
   // folded rows: fragments of the current and the next stage
   u32x4 xcur[4], xnext[4];

@@ -152,13 +152,21 @@ int make_orth_plan(int32_t E, int32_t M, int32_t N, OrthPlan* p) {
   p->n = M < N ? N : M;
   p->tall = M > N;
   if ((int64_t)M * N * 4 >= kLim31 || (int64_t)p->m * p->m * 4 >= kLim31) return MOE_ERR_UNSUPPORTED;
+  const int64_t mn = (int64_t)M * N;
+  int s = 0;  // S = 2^ceil(log2 sqrt(M N)), at most 2^15
+  while (s < 15 && (int64_t(1) << (2 * s)) < mn) ++s;
+  p->scale = (float)(1 << s);
+  const int64_t blocks = (mn + 16383) / 16384;  // eight passes of 256 threads x 8 values
+  p->norm_parts = blocks < 128 ? (int)blocks : 128;
   Layout l;
-  const size_t mn = sizeof(float) * (size_t)E * M * N, mm = sizeof(float) * (size_t)E * p->m * p->m;
-  p->off_x[0] = l.take(mn);
-  p->off_x[1] = l.take(mn);
+  const size_t x = 2 * (size_t)E * M * N, mm = 2 * (size_t)E * p->m * p->m;
+  p->off_hi[0] = l.take(x);
+  p->off_hi[1] = l.take(x);
+  p->off_lo = l.take(x);
   p->off_p = l.take(mm);
   p->off_q = l.take(mm);
-  p->off_norm = l.take(sizeof(float) * E);
+  p->off_norm = l.take(sizeof(double) * E * p->norm_parts);
+  p->off_partial = l.take(E ? sizeof(float) * kOrthPartialFloats : 0);
   p->total = l.o;
   return MOE_OK;
 }

@@ -51,12 +51,17 @@ struct LoraBwdPlan {
 };
 int make_lora_backward_plan(const moe_lora_shape* s, LoraBwdPlan* p);
 
+constexpr int64_t kOrthPartialFloats = int64_t(256) * 65536;  // 64 MB of partial tiles
 struct OrthPlan {
-  int m, n;        // the smaller and the larger side
-  int tall;        // M > N: P = X^T X
-  size_t off_x[2]; // fp32 [E][M][N]
-  size_t off_p, off_q;
-  size_t off_norm;
+  int m, n;           // the smaller and the larger side
+  int tall;           // M > N: P = X^T X
+  float scale;        // S: fp16 X holds S X
+  int norm_parts;     // blocks per matrix of the sum of squares
+  size_t off_hi[2];   // fp16 [E][M][N]: X's upper part, this step's and the next's
+  size_t off_lo;      // fp16 [E][M][N]: its lower part
+  size_t off_p, off_q;  // fp16 [E][m][m]
+  size_t off_norm;    // double [E][norm_parts]
+  size_t off_partial; // fp32 partial tiles
   size_t total;
 };
 int make_orth_plan(int32_t E, int32_t M, int32_t N, OrthPlan* p);

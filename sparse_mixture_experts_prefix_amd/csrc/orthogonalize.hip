@@ -1,102 +1,591 @@
 // Orthogonalised updates by Newton-Schulz products (moe_orthogonalize in moe.h).
-#include "device.hpp"
+//
+// Per step and matrix, m the smaller side, n the larger:
+//   P = X X^T (or X^T X)      symmetric, m^2 n multiply-adds, half of them needed
+//   Q = b P + c P P           symmetric, m^3, half needed
+//   X' = a X + Q X (or X Q)   m^2 n
+// Every product runs on MFMA tiles (256 x 256 x 64 with the K loop of gemm_tile.hpp;
+// 128 x 128 x 64 where those would leave most CUs idle) in the layout X has: rows
+// or columns as the reduction, so nothing is transposed.  The symmetric ones
+// compute the tiles on and below the diagonal and store each twice.
+//
+// Numbers.  Operands are fp16 (11 bits; bf16's 8 showed 1 to 17% error on
+// gradients of falling singular values) with power-of-two scales: X times
+// S = 2^ceil(log2 sqrt(M N)) (at most 2^15: |X| stays below about 1.2), P and Q
+// times SP = 2^13 (|P| <= 1.45, |Q| <= 2.81).  X is carried in two fp16 parts:
+// the products read the upper one, and the step adds a (hi + lo), so the rounding of
+// X does not feed the directions that later steps amplify by up to 3.4 each
+// (with one part 1.5 to 5% error on such gradients, with two 0.2 to 0.4%,
+// most of it the bf16 result's own rounding).
+#include "gemm_tile.hpp"
+#include "launch.hpp"
 #include "ops_launch.hpp"
-#include "simple_tile.hpp"
+#include "ragged.hpp"
 
 namespace moe {
 namespace {
 
-constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+typedef _Float16 f16;
+typedef f16 f16x2 __attribute__((ext_vector_type(2)));
+typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kSP = 8192.f;
+
+// -------------------------------------------------------- norm and first X
 __device__ __forceinline__ float g_at(const void* g, int dtype, int64_t i) {
   return dtype == MOE_DTYPE_F32 ? static_cast<const float*>(g)[i]
                                 : bf16_to_f32(static_cast<const bf16_t*>(g)[i]);
 }
 
-// norm[e] = |G_e|_F, summed in double so that no gradient's squares under- or overflow
-__global__ __launch_bounds__(256) void moe_orth_norm_kernel(const void* g, int dtype, int64_t mn, float* norm) {
-  __shared__ double sum[256];
-  const int64_t base = blockIdx.x * mn;
+// eight consecutive values (the matrices' sizes are multiples of 8)
+__device__ __forceinline__ void load8(const void* g, int dtype, int64_t i, float (&v)[8]) {
+  if (dtype == MOE_DTYPE_F32) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(g) + i);
+    const float4 a = q[0], b = q[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const u32x4 q = ld16(static_cast<const bf16_t*>(g) + i);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      v[2 * h] = __builtin_bit_cast(float, q[h] << 16);
+      v[2 * h + 1] = __builtin_bit_cast(float, q[h] & 0xFFFF0000u);
+    }
+  }
+}
+
+// part[e][b] = sum of squares of block b's share of matrix e, in double so that no
+// gradient's squares under- or overflow; fixed order.  Bound by reading G.
+__global__ __launch_bounds__(256) void moe_orth_norm_kernel(const void* g, int dtype, int64_t mn, double* part) {
+  __shared__ double sum[4];
+  const int64_t base = (int64_t)blockIdx.y * mn;
   double s = 0;
-  for (int64_t i = threadIdx.x; i < mn; i += 256) {
-    const double v = g_at(g, dtype, base + i);
-    s += v * v;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < mn; i += (int64_t)gridDim.x * 2048) {
+    float v[8];
+    load8(g, dtype, base + i, v);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s = fma((double)v[u], (double)v[u], s);
   }
-  sum[threadIdx.x] = s;
+  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
+  if ((threadIdx.x & 63) == 0) sum[threadIdx.x >> 6] = s;
   __syncthreads();
-  for (int o = 128; o; o >>= 1) {
-    if (threadIdx.x < o) sum[threadIdx.x] += sum[threadIdx.x + o];
-    __syncthreads();
+  if (threadIdx.x == 0)
+    part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = ((sum[0] + sum[1]) + sum[2]) + sum[3];
+}
+
+// hi + lo = S G / (|G| + eps), zeros for a matrix of zeros
+__global__ __launch_bounds__(256) void moe_orth_scale_kernel(const void* g, int dtype, int64_t mn,
+                                                             const double* part, int parts, float eps,
+                                                             float S, f16* hi, f16* lo) {
+  const int64_t e = blockIdx.y;
+  double s = 0;
+  for (int b = 0; b < parts; ++b) s += part[e * parts + b];
+  const double d = sqrt(s) + (double)eps;
+  const double f = d > 0 ? (double)S / d : 0.0 * d;  // NaN stays NaN
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < mn; i += (int64_t)gridDim.x * 2048) {
+    float v[8];
+    load8(g, dtype, e * mn + i, v);
+    f16x8 h, l;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float x = (float)((double)v[u] * f);
+      h[u] = (f16)x;
+      l[u] = (f16)(x - (float)h[u]);
+    }
+    *reinterpret_cast<f16x8*>(hi + e * mn + i) = h;
+    *reinterpret_cast<f16x8*>(lo + e * mn + i) = l;
   }
-  if (threadIdx.x == 0) norm[blockIdx.x] = (float)sqrt(sum[0]);
 }
 
-__global__ void moe_orth_scale_kernel(const void* g, int dtype, int64_t mn, const float* norm, float eps, float* x) {
-  const int64_t e = blockIdx.y, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= mn) return;
-  const float d = norm[e] + eps;
-  x[e * mn + i] = d > 0.f ? g_at(g, dtype, e * mn + i) / d : 0.f;
+// ----------------------------------------------------------------- products
+// C = A B^T per matrix, A: M rows, B: N rows of K values; row-major operands have
+// K contiguous ([rows][K]), K-major ones are [K][rows].  sym: C is symmetric (M = N).
+// Results: sym: d0 = alpha acc (+ beta c0 when set); else with v = alpha acc +
+// beta (c0 + c1): out = bf16(gamma v) when set, or d0 + d1 = v in two parts.
+struct OrthProduct {
+  const f16 *A, *B;
+  int64_t sA, sB;  // elements per matrix
+  int lda, ldb;
+  int M, N, K, sym;
+  int tm, tn, per;     // tiles down, across and per matrix
+  int64_t n_dp;        // tiles run whole (the first ones)
+  int R, S;            // tiles cut along K, pieces each
+  float* partial;      // [R][S][tile][tile]
+  const f16 *c0, *c1;
+  f16 *d0, *d1;
+  bf16_t* out;
+  float alpha, beta, gamma;
+};
+
+// Tile t of a matrix: m-tile, n-tile.  sym: the tiles on and below the diagonal, row
+// by row; a ragged last m-tile then meets every n-tile as the shorter operand.
+// Else blocks of 4 m-tiles x 8 n-tiles, m fastest, for operand reuse in L2.
+__device__ __forceinline__ void orth_coords(const OrthProduct& p, int t, int& i, int& j) {
+  if (p.sym) {
+    i = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
+    while (i * (i + 1) / 2 > t) --i;
+    while ((i + 1) * (i + 2) / 2 <= t) ++i;
+    j = t - i * (i + 1) / 2;
+    return;
+  }
+  const int col = t / (p.tm * 8), u = t - col * p.tm * 8;  // columns of 8 n-tiles
+  const int cw = min(8, p.tn - col * 8);
+  const int blk = u / (4 * cw), v = u - blk * 4 * cw;
+  const int mh = min(4, p.tm - blk * 4);
+  i = blk * 4 + v % mh;
+  j = col * 8 + v / mh;
 }
 
-// P = X X^T (tall: X^T X), one tile per block, z: matrix
-__global__ __launch_bounds__(256) void moe_orth_gram_kernel(const float* x, float* p, int m, int n, int tall) {
-  const float* X = x + (int64_t)blockIdx.z * m * n;
-  float* P = p + (int64_t)blockIdx.z * m * m;
-  auto a = [&](int64_t i, int64_t k) { return tall ? X[k * m + i] : X[i * n + k]; };
-  auto st = [&](int64_t i, int64_t j, float v) { P[i * m + j] = v; };
-  simple_tile(a, a, st, m, m, n, (int64_t)blockIdx.y * 64, (int64_t)blockIdx.x * 64);
+struct OrthTile {
+  int e, m0, n0, s0, s1;  // matrix, corner, K stages [s0, s1)
+  int piece;              // index of the partial tile, or -1
+};
+
+// Workgroup b's tile: whole tiles in 8 runs, one per XCD (workgroup b runs on XCD
+// b % 8), then the pieces.  False: nothing to do.
+template <int TS>
+__device__ __forceinline__ bool orth_tile(const OrthProduct& p, int64_t b, OrthTile& t) {
+  const int64_t run = (p.n_dp + 7) / 8;
+  int64_t L;
+  int part = 0;
+  t.piece = -1;
+  if (b < 8 * run) {
+    L = (b % 8) * run + b / 8;
+    if (L >= p.n_dp) return false;
+  } else {
+    const int64_t q = b - 8 * run;
+    if (q >= (int64_t)p.R * p.S) return false;
+    L = p.n_dp + q % p.R;
+    part = (int)(q / p.R);
+    t.piece = (int)(q % p.R) * p.S + part;
+  }
+  t.e = (int)(L / p.per);
+  int i, j;
+  orth_coords(p, (int)(L - (int64_t)t.e * p.per), i, j);
+  t.m0 = i * TS;
+  t.n0 = j * TS;
+  const int nk = (p.K + BK - 1) / BK;
+  t.s0 = t.piece < 0 ? 0 : (int)((int64_t)part * nk / p.S);
+  t.s1 = t.piece < 0 ? nk : (int)((int64_t)(part + 1) * nk / p.S);
+  return true;
 }
 
-// Q = b P + c P P
-__global__ __launch_bounds__(256) void moe_orth_poly_kernel(const float* p, float* q, int m) {
-  const float* P = p + (int64_t)blockIdx.z * m * m;
-  float* Q = q + (int64_t)blockIdx.z * m * m;
-  auto a = [&](int64_t i, int64_t k) { return P[i * m + k]; };
-  auto st = [&](int64_t i, int64_t j, float v) { Q[i * m + j] = kB * P[i * m + j] + kC * v; };
-  simple_tile(a, a, st, m, m, m, (int64_t)blockIdx.y * 64, (int64_t)blockIdx.x * 64);
+// Results of a 32 x 32 block at (m, n): register r of lane l is row 8 (r / 4) +
+// 4 (l / 32) + r % 4, column l % 32.  Register pairs hold two rows of a column;
+// neighbouring lanes swap one value so that each lane has two columns of a row
+// (4-byte loads and stores).  mirror: also stored transposed, four rows of a
+// column as 8 bytes.
+__device__ __forceinline__ void orth_store(const OrthProduct& p, int64_t at, int m, int n, int lane,
+                                           const f32x16& acc, bool mirror) {
+  const int lr = lane & 31, kh = lane >> 5;
+  const bool odd = lane & 1;
+  const int c = n + (lr & ~1);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float v0 = acc[2 * q], v1 = acc[2 * q + 1];
+    const float send = odd ? v0 : v1;
+    const float got = __builtin_bit_cast(
+        float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, send), 0xB1, 0xF, 0xF, false));
+    float x = (odd ? got : v0) * p.alpha, y = (odd ? v1 : got) * p.alpha;
+    const int r = 2 * q + (odd ? 1 : 0);
+    const int row = m + 8 * (r >> 2) + 4 * kh + (r & 3);
+    if (row >= p.M || c >= p.N) continue;
+    const int64_t i = at + (int64_t)row * p.N + c;
+    if (p.c0) {
+      const f16x2 h = *reinterpret_cast<const f16x2*>(p.c0 + i);
+      float hx = h[0], hy = h[1];
+      if (p.c1) {
+        const f16x2 l = *reinterpret_cast<const f16x2*>(p.c1 + i);
+        hx += (float)l[0];
+        hy += (float)l[1];
+      }
+      x = fmaf(p.beta, hx, x);
+      y = fmaf(p.beta, hy, y);
+    }
+    if (p.out) {
+      const uint32_t w = (uint32_t)f32_to_bf16(x * p.gamma) | ((uint32_t)f32_to_bf16(y * p.gamma) << 16);
+      *reinterpret_cast<uint32_t*>(p.out + i) = w;
+      continue;
+    }
+    const f16x2 h{(f16)x, (f16)y};
+    *reinterpret_cast<f16x2*>(p.d0 + i) = h;
+    if (p.d1) *reinterpret_cast<f16x2*>(p.d1 + i) = f16x2{(f16)(x - (float)h[0]), (f16)(y - (float)h[1])};
+  }
+  if (!mirror) return;
+  const int col = n + lr;
+  if (col >= p.N) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int row = m + 8 * q + 4 * kh;
+    if (row >= p.M) continue;  // M is a multiple of 8: four rows are in or out together
+    f16x4 v;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float x = acc[4 * q + u] * p.alpha;
+      if (p.c0) x = fmaf(p.beta, (float)p.c0[at + (int64_t)(row + u) * p.N + col], x);
+      v[u] = (f16)x;
+    }
+    *reinterpret_cast<f16x4*>(p.d0 + at + (int64_t)col * p.N + row) = v;
+  }
 }
 
-// X' = a X + Q X (tall: a X + X Q)
-__global__ __launch_bounds__(256) void moe_orth_apply_kernel(const float* x, const float* q, float* xo,
-                                                             bf16_t* out, int m, int n, int tall) {
-  const float* X = x + (int64_t)blockIdx.z * m * n;
-  const float* Q = q + (int64_t)blockIdx.z * m * m;
-  const int64_t rows = tall ? n : m, cols = tall ? m : n, at0 = (int64_t)blockIdx.z * m * n;
-  auto a = [&](int64_t i, int64_t k) { return tall ? X[i * m + k] : Q[i * m + k]; };
-  auto b = [&](int64_t j, int64_t k) { return tall ? Q[j * m + k] : X[k * n + j]; };
-  auto st = [&](int64_t i, int64_t j, float v) {
-    const int64_t at = i * cols + j;
-    v += kA * X[at];
-    if (out)
-      out[at0 + at] = f32_to_bf16(v);
+// 256 x 256 tiles.  KB: B is K-major, KA: A is too.
+template <bool KA, bool KB>
+__global__ __launch_bounds__(256) void moe_orth_tile256_kernel(OrthProduct p) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  OrthTile t;
+  if (!orth_tile<256>(p, blockIdx.x, t)) return;
+  const int lane = threadIdx.x & 63, sub = lane >> 3;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int valid = min(256, p.M - t.m0);
+  const __amdgpu_buffer_rsrc_t rsA =
+      make_rsrc(p.A + t.e * p.sA, (uint32_t)((KA ? p.K : p.M) * p.lda * 2));
+  const __amdgpu_buffer_rsrc_t rsB =
+      make_rsrc(p.B + t.e * p.sB, (uint32_t)((KB ? p.K : p.N) * p.ldb * 2));
+  // load slots as in prefill_tile (rows) and wgrad_issue (K-major)
+  uint32_t offA[8], offB[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int kr = 2 * (wave * 8 + j) + (lane >> 5), kc = 8 * kmaj_chunk(kr, lane & 31);
+    const int ra = (j * 4 + wave) * 8 + sub, rb = (wave * 8 + j) * 8 + sub;
+    if (KA)
+      offA[j] = t.m0 + kc < p.M ? (uint32_t)((kr * p.lda + t.m0 + kc) * 2) : kOob;
     else
-      xo[at0 + at] = v;
+      offA[j] = ra < valid ? (uint32_t)(((t.m0 + ra) * p.lda + 8 * ((lane & 7) ^ swz(ra))) * 2) : kOob;
+    if (KB)
+      offB[j] = t.n0 + kc < p.N ? (uint32_t)((kr * p.ldb + t.n0 + kc) * 2) : kOob;
+    else
+      offB[j] = t.n0 + rb < p.N ? (uint32_t)(((t.n0 + rb) * p.ldb + 8 * ((lane & 7) ^ swz(rb))) * 2) : kOob;
+  }
+  auto issue = [&](bool isB, int stage, int buf, int j0, int j1) {
+    const int k0 = stage * BK;
+    const bool kmaj = isB ? KB : KA;
+    const bool tail = k0 + BK > p.K;
+    char* base = isB ? lds + 2 * kABytes + buf * kBBytes : lds + buf * kABytes;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j < j0 || j >= j1) continue;
+      uint32_t o = isB ? offB[j] : offA[j];
+      const int blk = isB || kmaj ? wave * 8 + j : j * 4 + wave;
+      if (tail) {
+        if (kmaj) {
+          if (k0 + 2 * (wave * 8 + j) + (lane >> 5) >= p.K) o = kOob;
+        } else if (k0 + 8 * ((lane & 7) ^ swz(blk * 8 + sub)) >= p.K) {
+          o = kOob;
+        }
+      }
+      const uint32_t soff = (uint32_t)(kmaj ? k0 * (isB ? p.ldb : p.lda) * 2 : k0 * 2);
+      if (KA || KB)
+        lds_dma16(isB ? rsB : rsA, base + blk * 1024, o, soff);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(isB ? rsB : rsA, (lds_void*)(base + blk * 1024), 16, o,
+                                                 (int)soff, 0, 0);
+    }
   };
-  simple_tile(a, b, st, rows, cols, m, (int64_t)blockIdx.y * 64, (int64_t)blockIdx.x * 64);
+  auto issue_a = [&](int stage, int buf, int j0, int j1) { issue(false, stage, buf, j0, j1); };
+  auto issue_b = [&](int stage, int buf, int j0, int j1) { issue(true, stage, buf, j0, j1); };
+  f32x16 acc[4][4];
+  zero_acc(acc);
+  const int n = t.s1 - t.s0;
+  const bool il = !KA && valid < 256;
+  int act = 4;
+  if constexpr (KA) {
+    k_loop<false, 4, false, decltype(issue_a), decltype(issue_b), true, true, false, 8, false, 0, true>(
+        lds, t.s0, n, wm, wn, il, lane, issue_a, issue_b, acc);
+  } else {
+    // a ragged last m-tile skips the loads and products of its missing rows (see prefill_tile)
+    if (il) act = min(4, max(0, ((valid + 31) / 32 - wm + 1) / 2));
+    const int tier = min(4, max(1, (valid + 63) / 64));
+#define MOE_KL(A_, N_)                                                                             \
+  k_loop<false, A_, false, decltype(issue_a), decltype(issue_b), KB, false, false, N_, false, 0, true>( \
+      lds, t.s0, n, wm, wn, il, lane, issue_a, issue_b, acc)
+    switch (tier * 8 + act) {
+      case 4 * 8 + 4: MOE_KL(4, 8); break;
+      case 4 * 8 + 3: MOE_KL(3, 8); break;
+      case 3 * 8 + 3: MOE_KL(3, 6); break;
+      case 3 * 8 + 2: MOE_KL(2, 6); break;
+      case 2 * 8 + 2: MOE_KL(2, 4); break;
+      case 2 * 8 + 1: MOE_KL(1, 4); break;
+      case 1 * 8 + 1: MOE_KL(1, 2); break;
+      default: MOE_KL(0, 2); break;
+    }
+#undef MOE_KL
+  }
+  const int lr = lane & 31, kh = lane >> 5;
+  if (t.piece >= 0) {
+    float* P = p.partial + (int64_t)t.piece * 65536;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= act) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          P[(a_row_of(wm, i, il) + 8 * (r >> 2) + 4 * kh + (r & 3)) * 256 + b_row_of<false>(wn, j) + lr] =
+              acc[i][j][r];
+    }
+    return;
+  }
+  const int64_t at = (int64_t)t.e * p.M * p.N;
+  const bool mirror = p.sym && t.m0 != t.n0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >= act) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      orth_store(p, at, t.m0 + a_row_of(wm, i, il), t.n0 + b_row_of<false>(wn, j), lane, acc[i][j], mirror);
+  }
+}
+
+// 128 x 128 tiles: 4 waves of 64 x 64 (2 x 2 MFMA blocks), three K stages of 32 KB
+// in LDS, two of them in flight.  Two workgroups share a CU's registers but not its
+// LDS; taken where the 256 x 256 tiles are too few for the chip.
+constexpr int kStage128 = 2 * 128 * BK * 2;
+template <bool KA, bool KB>
+__global__ __launch_bounds__(256) void moe_orth_tile128_kernel(OrthProduct p) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  OrthTile t;
+  if (!orth_tile<128>(p, blockIdx.x, t)) return;
+  const int lane = threadIdx.x & 63, sub = lane >> 3;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int lr = lane & 31, kh = lane >> 5;
+  const __amdgpu_buffer_rsrc_t rsA =
+      make_rsrc(p.A + t.e * p.sA, (uint32_t)((KA ? p.K : p.M) * p.lda * 2));
+  const __amdgpu_buffer_rsrc_t rsB =
+      make_rsrc(p.B + t.e * p.sB, (uint32_t)((KB ? p.K : p.N) * p.ldb * 2));
+  // a stage's operand is 16 blocks of 1 KB, four per wave: 8 rows of 128 bytes, or
+  // (K-major) 4 k-rows of 256 bytes, whose chunk c sits at c ^ 4 (k % 4) as kmaj_chunk's
+  auto issue_op = [&](const __amdgpu_buffer_rsrc_t rs, bool kmaj, int r0, int rows, int ld, int stage, char* st) {
+    const int k0 = stage * BK;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int blk = wave * 4 + j;
+      uint32_t o;
+      if (kmaj) {
+        const int k = k0 + 4 * blk + (lane >> 4), c = r0 + 8 * kmaj_chunk(4 * blk + (lane >> 4), lane & 15);
+        o = k < p.K && c < rows ? (uint32_t)((k * ld + c) * 2) : kOob;
+      } else {
+        const int r = blk * 8 + sub, k = k0 + 8 * ((lane & 7) ^ swz(r));
+        o = k < p.K && r0 + r < rows ? (uint32_t)(((r0 + r) * ld + k) * 2) : kOob;
+      }
+      lds_dma16(rs, st + blk * 1024, o, 0);
+    }
+  };
+  auto issue = [&](int stage, int buf) {
+    char* st = lds + __builtin_amdgcn_readfirstlane(buf * kStage128);
+    issue_op(rsA, KA, t.m0, p.M, p.lda, stage, st);
+    issue_op(rsB, KB, t.n0, p.N, p.ldb, stage, st + kStage128 / 2);
+  };
+  typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+  typedef __attribute__((address_space(3))) char lds_char;
+  auto read = [&](const char* st, bool kmaj, int r0, int ks) {
+    if (kmaj) {
+      const int q = lane & 15, k = 16 * ks + 8 * kh + (q >> 2), c = r0 + 16 * ((lane >> 4) & 1) + 4 * (q & 3);
+      const char* at = st + k * 256 + kmaj_chunk(k, c >> 3) * 16 + (c & 7) * 2;
+      const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)((lds_char*)at));
+      const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)((lds_char*)(at + 4 * 256)));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    const int r = r0 + lr;
+    return *reinterpret_cast<const bf16x8*>(st + r * 128 + ((2 * ks + kh) ^ swz(r)) * 16);
+  };
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  const int n = t.s1 - t.s0;
+  issue(t.s0, 0);
+  if (n > 1) issue(t.s0 + 1, 1);
+  int buf = 0;
+  for (int s = 0; s < n; ++s) {
+    if (s + 1 < n)
+      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // stage s landed, s + 1 may fly
+    else
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();  // every wave's part of stage s; all have left stage s - 1
+    asm volatile("" ::: "memory");
+    const int b2 = buf == 0 ? 2 : buf - 1;
+    if (s + 2 < n) issue(t.s0 + s + 2, b2);
+    const char* sa = lds + buf * kStage128;
+    const char* sb = sa + kStage128 / 2;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      bf16x8 a[2], b[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) a[i] = read(sa, KA, wm * 64 + 32 * i, ks);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) b[j] = read(sb, KB, wn * 64 + 32 * j, ks);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<true>(a[i], b[j], acc[i][j]);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of stage s are done
+    buf = buf == 2 ? 0 : buf + 1;
+  }
+  if (t.piece >= 0) {
+    float* P = p.partial + (int64_t)t.piece * 16384;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          P[(wm * 64 + 32 * i + 8 * (r >> 2) + 4 * kh + (r & 3)) * 128 + wn * 64 + 32 * j + lr] = acc[i][j][r];
+    return;
+  }
+  const int64_t at = (int64_t)t.e * p.M * p.N;
+  const bool mirror = p.sym && t.m0 != t.n0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      orth_store(p, at, t.m0 + wm * 64 + 32 * i, t.n0 + wn * 64 + 32 * j, lane, acc[i][j], mirror);
+}
+
+// Finishes the cut tiles: one wave per 32 x 32 block, in the registers' layout of
+// an MFMA block; the pieces are added in K order.
+template <int TS>
+__global__ __launch_bounds__(64) void moe_orth_fixup_kernel(OrthProduct p) {
+  constexpr int NB = TS / 32;
+  const int tile = blockIdx.x / (NB * NB), blk = blockIdx.x % (NB * NB);
+  const int64_t L = p.n_dp + tile;
+  const int e = (int)(L / p.per);
+  int ti, tj;
+  orth_coords(p, (int)(L - (int64_t)e * p.per), ti, tj);
+  const int m = 32 * (blk / NB), n = 32 * (blk % NB), lane = threadIdx.x;
+  if (ti * TS + m >= p.M || tj * TS + n >= p.N) return;
+  const float* P = p.partial + (int64_t)tile * p.S * TS * TS + (m + 4 * (lane >> 5)) * TS + n + (lane & 31);
+  f32x16 acc;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[r] = P[(8 * (r >> 2) + (r & 3)) * TS];
+  for (int s = 1; s < p.S; ++s) {
+    P += TS * TS;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] += P[(8 * (r >> 2) + (r & 3)) * TS];
+  }
+  orth_store(p, (int64_t)e * p.M * p.N, ti * TS + m, tj * TS + n, lane, acc, p.sym && ti != tj);
+}
+
+template <int TS, bool KA, bool KB>
+hipError_t launch_tiles(const OrthProduct& p, hipStream_t s) {
+  static std::atomic<uint64_t> done;
+  constexpr int lds = TS == 256 ? kLdsBytes : 3 * kStage128;
+  void (*kernel)(OrthProduct);
+  if constexpr (TS == 256)
+    kernel = moe_orth_tile256_kernel<KA, KB>;
+  else
+    kernel = moe_orth_tile128_kernel<KA, KB>;
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), lds, done);
+  if (e != hipSuccess) return e;
+  const int64_t blocks = (p.n_dp + 7) / 8 * 8 + (int64_t)p.R * p.S;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), lds, s, p);
+  if (p.R)
+    hipLaunchKernelGGL(moe_orth_fixup_kernel<TS>, dim3((unsigned)(p.R * (TS / 32) * (TS / 32))), dim3(64), 0, s, p);
+  return hipGetLastError();
+}
+
+// Tile size, and which tiles are cut along K (E matrices; ctas CUs).
+template <bool KA, bool KB>
+hipError_t launch_product(OrthProduct p, int E, int ctas, hipStream_t s) {
+  auto tiles = [&](int ts) {
+    p.tm = (p.M + ts - 1) / ts;
+    p.tn = (p.N + ts - 1) / ts;
+    p.per = p.sym ? p.tm * (p.tm + 1) / 2 : p.tm * p.tn;
+    return (int64_t)E * p.per;
+  };
+  // half the chip's CUs with 256 x 256 tiles, or smaller ones that reach more CUs
+  int64_t V = tiles(256);
+  const int ts = V * 2 >= ctas ? 256 : 128;
+  if (ts == 128) V = tiles(128);
+  // the partial last round, cut along K in pieces of at least 4 stages
+  const int64_t rounds = V / ctas;
+  int64_t R = V % ctas;
+  const int64_t by_k = ((p.K + BK - 1) / BK) / kMinPieceStages;
+  int64_t S = R ? ctas / R : 1;
+  if (S > by_k) S = by_k;
+  if (S > 16) S = 16;
+  if (S < 2 || rounds >= kSplitRounds || R * S * ts * ts > kOrthPartialFloats) R = 0, S = 1;
+  p.n_dp = V - R;
+  p.R = (int)R;
+  p.S = (int)S;
+  return ts == 256 ? launch_tiles<256, KA, KB>(p, s) : launch_tiles<128, KA, KB>(p, s);
 }
 
 }  // namespace
 
-hipError_t launch_orthogonalize(int E, int M, int N, const OrthPlan& p, const void* g, int g_dtype,
+hipError_t launch_orthogonalize(int E, int M, int N, const OrthPlan& plan, const void* g, int g_dtype,
                                 int steps, float eps, void* out, void* ws, hipStream_t st) {
   char* w = static_cast<char*>(ws);
-  float* x[2] = {reinterpret_cast<float*>(w + p.off_x[0]), reinterpret_cast<float*>(w + p.off_x[1])};
-  float* P = reinterpret_cast<float*>(w + p.off_p);
-  float* Q = reinterpret_cast<float*>(w + p.off_q);
-  float* norm = reinterpret_cast<float*>(w + p.off_norm);
+  f16* hi[2] = {reinterpret_cast<f16*>(w + plan.off_hi[0]), reinterpret_cast<f16*>(w + plan.off_hi[1])};
+  f16* lo = reinterpret_cast<f16*>(w + plan.off_lo);
+  f16* P = reinterpret_cast<f16*>(w + plan.off_p);
+  f16* Q = reinterpret_cast<f16*>(w + plan.off_q);
+  double* part = reinterpret_cast<double*>(w + plan.off_norm);
+  int ctas = 0;
+  hipError_t e = split_ctas(&ctas);
+  if (e != hipSuccess) return e;
   const int64_t mn = (int64_t)M * N;
-  const unsigned tm = (p.m + 63) / 64;
-  hipLaunchKernelGGL(moe_orth_norm_kernel, dim3(E), dim3(256), 0, st, g, g_dtype, mn, norm);
-  hipLaunchKernelGGL(moe_orth_scale_kernel, dim3((unsigned)((mn + 255) / 256), E), dim3(256), 0, st, g,
-                     g_dtype, mn, norm, eps, x[0]);
-  for (int i = 0; i < steps; ++i) {
-    hipLaunchKernelGGL(moe_orth_gram_kernel, dim3(tm, tm, E), dim3(256), 0, st, x[i & 1], P, p.m, p.n, p.tall);
-    hipLaunchKernelGGL(moe_orth_poly_kernel, dim3(tm, tm, E), dim3(256), 0, st, P, Q, p.m);
-    hipLaunchKernelGGL(moe_orth_apply_kernel, dim3((N + 63) / 64, (M + 63) / 64, E), dim3(256), 0, st,
-                       x[i & 1], Q, x[~i & 1], i + 1 == steps ? static_cast<bf16_t*>(out) : nullptr, p.m,
-                       p.n, p.tall);
+  const int m = plan.m, n = plan.n;
+  const float S = plan.scale;
+  const dim3 grid((unsigned)plan.norm_parts, (unsigned)E);
+  hipLaunchKernelGGL(moe_orth_norm_kernel, grid, dim3(256), 0, st, g, g_dtype, mn, part);
+  const int64_t sb = (mn / 8 + 255) / 256;
+  hipLaunchKernelGGL(moe_orth_scale_kernel, dim3((unsigned)(sb < 1024 ? sb : 1024), (unsigned)E), dim3(256), 0, st,
+                     g, g_dtype, mn, part, plan.norm_parts, eps, S, hi[0], lo);
+  e = hipGetLastError();
+  for (int i = 0; i < steps && e == hipSuccess; ++i) {
+    const f16* X = hi[i & 1];
+    OrthProduct gram{};
+    gram.A = gram.B = X;
+    gram.sA = gram.sB = mn;
+    gram.lda = gram.ldb = N;
+    gram.M = gram.N = m;
+    gram.K = n;
+    gram.sym = 1;
+    gram.partial = reinterpret_cast<float*>(w + plan.off_partial);
+    gram.d0 = P;
+    gram.alpha = kSP / (S * S);
+    e = plan.tall ? launch_product<true, true>(gram, E, ctas, st)
+                  : launch_product<false, false>(gram, E, ctas, st);
+    OrthProduct poly = gram;
+    poly.A = poly.B = P;
+    poly.sA = poly.sB = (int64_t)m * m;
+    poly.lda = poly.ldb = poly.K = m;
+    poly.d0 = Q;
+    poly.alpha = kC / kSP;
+    poly.c0 = P;
+    poly.beta = kB;
+    if (e == hipSuccess) e = launch_product<false, false>(poly, E, ctas, st);
+    OrthProduct step = poly;
+    step.sym = 0;
+    step.M = M;
+    step.N = N;
+    step.K = m;
+    step.A = plan.tall ? X : Q;
+    step.sA = plan.tall ? mn : (int64_t)m * m;
+    step.lda = m;
+    step.B = plan.tall ? Q : X;
+    step.sB = plan.tall ? (int64_t)m * m : mn;
+    step.ldb = N;  // tall: N = m
+    step.c0 = X;
+    step.c1 = lo;
+    step.d0 = hi[~i & 1];
+    step.d1 = lo;
+    step.out = i + 1 == steps ? static_cast<bf16_t*>(out) : nullptr;
+    step.alpha = 1.f / kSP;
+    step.beta = kA;
+    step.gamma = 1.f / S;
+    if (e == hipSuccess)
+      e = plan.tall ? launch_product<false, false>(step, E, ctas, st)
+                    : launch_product<false, true>(step, E, ctas, st);
   }
-  return hipGetLastError();
+  return e;
 }
 
 }  // namespace moe

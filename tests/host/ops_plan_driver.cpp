@@ -41,7 +41,8 @@ int main() {
           moe::OrthPlan o;
           if (moe::make_orth_plan(g, n, k, &o) == 0) {
             ++accepted;
-            if (!ordered({o.off_x[0], o.off_x[1], o.off_p, o.off_q, o.off_norm}, o.total)) return 5;
+            if (!ordered({o.off_hi[0], o.off_hi[1], o.off_lo, o.off_p, o.off_q, o.off_norm, o.off_partial},
+                         o.total)) return 5;
           }
         }
   std::printf("%ld\n", accepted);

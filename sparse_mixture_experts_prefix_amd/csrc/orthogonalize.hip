@@ -26,8 +26,6 @@ namespace moe {
 namespace {
 
 typedef _Float16 f16;
-typedef f16 f16x2 __attribute__((ext_vector_type(2)));
-typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kSP = 8192.f;
@@ -170,62 +168,66 @@ __device__ __forceinline__ bool orth_tile(const OrthProduct& p, int64_t b, OrthT
   return true;
 }
 
-// Results of a 32 x 32 block at (m, n): register r of lane l is row 8 (r / 4) +
-// 4 (l / 32) + r % 4, column l % 32.  Register pairs hold two rows of a column;
-// neighbouring lanes swap one value so that each lane has two columns of a row
-// (4-byte loads and stores).  mirror: also stored transposed, four rows of a
-// column as 8 bytes.
-__device__ __forceinline__ void orth_store(const OrthProduct& p, int64_t at, int m, int n, int lane,
-                                           const f32x16& acc, bool mirror) {
-  const int lr = lane & 31, kh = lane >> 5;
-  const bool odd = lane & 1;
-  const int c = n + (lr & ~1);
+// Eight results v of row `row`, columns col .. col + 7: all of a result's reads
+// and writes are 16 bytes wide.
+__device__ __forceinline__ void emit_row(const OrthProduct& p, int64_t at, int row, int col, float (&v)[8]) {
+  const int64_t i = at + (int64_t)row * p.N + col;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const float v0 = acc[2 * q], v1 = acc[2 * q + 1];
-    const float send = odd ? v0 : v1;
-    const float got = __builtin_bit_cast(
-        float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, send), 0xB1, 0xF, 0xF, false));
-    float x = (odd ? got : v0) * p.alpha, y = (odd ? v1 : got) * p.alpha;
-    const int r = 2 * q + (odd ? 1 : 0);
-    const int row = m + 8 * (r >> 2) + 4 * kh + (r & 3);
-    if (row >= p.M || c >= p.N) continue;
-    const int64_t i = at + (int64_t)row * p.N + c;
-    if (p.c0) {
-      const f16x2 h = *reinterpret_cast<const f16x2*>(p.c0 + i);
-      float hx = h[0], hy = h[1];
-      if (p.c1) {
-        const f16x2 l = *reinterpret_cast<const f16x2*>(p.c1 + i);
-        hx += (float)l[0];
-        hy += (float)l[1];
-      }
-      x = fmaf(p.beta, hx, x);
-      y = fmaf(p.beta, hy, y);
-    }
-    if (p.out) {
-      const uint32_t w = (uint32_t)f32_to_bf16(x * p.gamma) | ((uint32_t)f32_to_bf16(y * p.gamma) << 16);
-      *reinterpret_cast<uint32_t*>(p.out + i) = w;
-      continue;
-    }
-    const f16x2 h{(f16)x, (f16)y};
-    *reinterpret_cast<f16x2*>(p.d0 + i) = h;
-    if (p.d1) *reinterpret_cast<f16x2*>(p.d1 + i) = f16x2{(f16)(x - (float)h[0]), (f16)(y - (float)h[1])};
+  for (int u = 0; u < 8; ++u) v[u] *= p.alpha;
+  if (p.c0) {
+    const f16x8 h = *reinterpret_cast<const f16x8*>(p.c0 + i);
+    f16x8 l;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) l[u] = (f16)0.f;
+    if (p.c1) l = *reinterpret_cast<const f16x8*>(p.c1 + i);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = fmaf(p.beta, (float)h[u] + (float)l[u], v[u]);
+  }
+  if (p.out) {
+    u32x4 w;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      w[u] = (uint32_t)f32_to_bf16(v[2 * u] * p.gamma) | ((uint32_t)f32_to_bf16(v[2 * u + 1] * p.gamma) << 16);
+    st16(p.out + i, w);
+    return;
+  }
+  f16x8 h, l;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    h[u] = (f16)v[u];
+    l[u] = (f16)(v[u] - (float)h[u]);
+  }
+  *reinterpret_cast<f16x8*>(p.d0 + i) = h;
+  if (p.d1) *reinterpret_cast<f16x8*>(p.d1 + i) = l;
+}
+
+// A tile of ROWS x TS results in LDS (fp32, rows of TS + 8 so that the lanes' column
+// and row accesses spread over the banks) at rows m, columns n of the result:
+// stored row by row, and (mirror) column by column as rows of the transposed place.
+// c0 is symmetric too, so the transposed place's own c0 serves there.
+template <int TS>
+constexpr int tile_pitch() { return TS + 8; }
+template <int ROWS, int TS>
+__device__ __forceinline__ void emit_tile(const OrthProduct& p, int64_t at, int m, int n, const float* tile,
+                                          bool mirror) {
+  const int rows = min(ROWS, p.M - m), cols = min(TS, p.N - n);  // multiples of 8
+  for (int q = threadIdx.x; q < ROWS * (TS / 8); q += 256) {
+    const int r = q / (TS / 8), c = q % (TS / 8) * 8;
+    if (r >= rows || c >= cols) continue;
+    float v[8];
+    const float4 a = *reinterpret_cast<const float4*>(tile + r * tile_pitch<TS>() + c);
+    const float4 b = *reinterpret_cast<const float4*>(tile + r * tile_pitch<TS>() + c + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    emit_row(p, at, m + r, n + c, v);
   }
   if (!mirror) return;
-  const int col = n + lr;
-  if (col >= p.N) return;
+  for (int q = threadIdx.x; q < TS * (ROWS / 8); q += 256) {
+    const int c = q % TS, r = q / TS * 8;
+    if (r >= rows || c >= cols) continue;
+    float v[8];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int row = m + 8 * q + 4 * kh;
-    if (row >= p.M) continue;  // M is a multiple of 8: four rows are in or out together
-    f16x4 v;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float x = acc[4 * q + u] * p.alpha;
-      if (p.c0) x = fmaf(p.beta, (float)p.c0[at + (int64_t)(row + u) * p.N + col], x);
-      v[u] = (f16)x;
-    }
-    *reinterpret_cast<f16x4*>(p.d0 + at + (int64_t)col * p.N + row) = v;
+    for (int u = 0; u < 8; ++u) v[u] = tile[(r + u) * tile_pitch<TS>() + c];
+    emit_row(p, at, n + c, m + r, v);
   }
 }
 
@@ -327,14 +329,26 @@ __global__ __launch_bounds__(256) void moe_orth_tile256_kernel(OrthProduct p) {
     }
     return;
   }
-  const int64_t at = (int64_t)t.e * p.M * p.N;
-  const bool mirror = p.sym && t.m0 != t.n0;
+  // the K loop's LDS takes the results, 128 rows at a time
+  float* tile = reinterpret_cast<float*>(lds);
+  static_assert(128 * tile_pitch<256>() * 4 <= kLdsBytes, "half a tile of results must fit");
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i >= act) continue;
+  for (int half = 0; half < 2; ++half) {
+    if (half * 128 >= valid) break;
+    __syncthreads();  // the K loop's reads, or the first half's, are done
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      orth_store(p, at, t.m0 + a_row_of(wm, i, il), t.n0 + b_row_of<false>(wn, j), lane, acc[i][j], mirror);
+    for (int i = 0; i < 4; ++i) {
+      const int row = a_row_of(wm, i, il) - 128 * half;
+      if (row < 0 || row >= 128) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          tile[(row + 8 * (r >> 2) + 4 * kh + (r & 3)) * tile_pitch<256>() + b_row_of<false>(wn, j) + lr] =
+              acc[i][j][r];
+    }
+    __syncthreads();
+    emit_tile<128, 256>(p, (int64_t)t.e * p.M * p.N, t.m0 + 128 * half, t.n0, tile, p.sym && t.m0 != t.n0);
   }
 }
 
@@ -439,37 +453,44 @@ __global__ __launch_bounds__(256) void moe_orth_tile128_kernel(OrthProduct p) {
           P[(wm * 64 + 32 * i + 8 * (r >> 2) + 4 * kh + (r & 3)) * 128 + wn * 64 + 32 * j + lr] = acc[i][j][r];
     return;
   }
-  const int64_t at = (int64_t)t.e * p.M * p.N;
-  const bool mirror = p.sym && t.m0 != t.n0;
+  float* tile = reinterpret_cast<float*>(lds);
+  static_assert(128 * tile_pitch<128>() * 4 <= 3 * kStage128, "the results must fit");
+  __syncthreads();  // the last stage's reads are done
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      orth_store(p, at, t.m0 + wm * 64 + 32 * i, t.n0 + wn * 64 + 32 * j, lane, acc[i][j], mirror);
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        tile[(wm * 64 + 32 * i + 8 * (r >> 2) + 4 * kh + (r & 3)) * tile_pitch<128>() + wn * 64 + 32 * j + lr] =
+            acc[i][j][r];
+  __syncthreads();
+  emit_tile<128, 128>(p, (int64_t)t.e * p.M * p.N, t.m0, t.n0, tile, p.sym && t.m0 != t.n0);
 }
 
-// Finishes the cut tiles: one wave per 32 x 32 block, in the registers' layout of
-// an MFMA block; the pieces are added in K order.
+// Finishes the cut tiles, 16 rows of one per workgroup: the pieces' sums are added
+// in K order.
 template <int TS>
-__global__ __launch_bounds__(64) void moe_orth_fixup_kernel(OrthProduct p) {
-  constexpr int NB = TS / 32;
-  const int tile = blockIdx.x / (NB * NB), blk = blockIdx.x % (NB * NB);
-  const int64_t L = p.n_dp + tile;
+__global__ __launch_bounds__(256) void moe_orth_fixup_kernel(OrthProduct p) {
+  __shared__ float tile[16 * tile_pitch<TS>()];
+  const int k = blockIdx.x / (TS / 16), r0 = blockIdx.x % (TS / 16) * 16;
+  const int64_t L = p.n_dp + k;
   const int e = (int)(L / p.per);
   int ti, tj;
   orth_coords(p, (int)(L - (int64_t)e * p.per), ti, tj);
-  const int m = 32 * (blk / NB), n = 32 * (blk % NB), lane = threadIdx.x;
-  if (ti * TS + m >= p.M || tj * TS + n >= p.N) return;
-  const float* P = p.partial + (int64_t)tile * p.S * TS * TS + (m + 4 * (lane >> 5)) * TS + n + (lane & 31);
-  f32x16 acc;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) acc[r] = P[(8 * (r >> 2) + (r & 3)) * TS];
-  for (int s = 1; s < p.S; ++s) {
-    P += TS * TS;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] += P[(8 * (r >> 2) + (r & 3)) * TS];
+  if (ti * TS + r0 >= p.M) return;
+  const float* P = p.partial + ((int64_t)k * p.S * TS + r0) * TS;
+  for (int q = threadIdx.x; q < 16 * TS / 4; q += 256) {
+    const float4* src = reinterpret_cast<const float4*>(P) + q;
+    float4 a = src[0];
+    for (int s = 1; s < p.S; ++s) {
+      const float4 b = src[(int64_t)s * TS * TS / 4];
+      a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+    }
+    *reinterpret_cast<float4*>(tile + q * 4 / TS * tile_pitch<TS>() + q * 4 % TS) = a;
   }
-  orth_store(p, (int64_t)e * p.M * p.N, ti * TS + m, tj * TS + n, lane, acc, p.sym && ti != tj);
+  __syncthreads();
+  emit_tile<16, TS>(p, (int64_t)e * p.M * p.N, ti * TS + r0, tj * TS, tile, p.sym && ti != tj);
 }
 
 template <int TS, bool KA, bool KB>
@@ -486,7 +507,7 @@ hipError_t launch_tiles(const OrthProduct& p, hipStream_t s) {
   const int64_t blocks = (p.n_dp + 7) / 8 * 8 + (int64_t)p.R * p.S;
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), lds, s, p);
   if (p.R)
-    hipLaunchKernelGGL(moe_orth_fixup_kernel<TS>, dim3((unsigned)(p.R * (TS / 32) * (TS / 32))), dim3(64), 0, s, p);
+    hipLaunchKernelGGL(moe_orth_fixup_kernel<TS>, dim3((unsigned)(p.R * (TS / 16))), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

@@ -88,6 +88,8 @@ _lock = threading.Lock()
 def load_library(path: str = LIB_PATH):
     """Load libmoe.so once; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -563,10 +565,20 @@ def _sized(fn, *args) -> int:
     return n.value
 
 
-def _workspace(workspace, nbytes, device):
+def _workspace(workspace, device, fn, *args):
+    """The caller's workspace (its size is the library's check), or a new one."""
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+        workspace = torch.empty(max(_sized(fn, *args), 1), dtype=torch.uint8, device=device)
     return _dev(workspace, "workspace", torch.uint8)
+
+
+def _run(device, fn, *args):
+    """Calls the library with `device` current, on its current stream."""
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(device.index)))
+        return
+    with torch.cuda.device(device):
+        _check(fn(*args, _stream(device)))
 
 
 def _gemm_shape(x, w, transposed, out_dtype) -> GemmShape:
@@ -609,15 +621,13 @@ def moe_grouped_gemm(x, offsets, w, *, w_scale=None, transposed=False, out_dtype
     elif w_scale is not None:
         raise ValueError("w_scale is only for uint8 (E4M3) weights")
     lib = load_library()
-    with torch.cuda.device(x.device):
-        if y is None:
-            y = torch.empty((shape.R, shape.N), dtype=out_dtype, device=x.device)
-        _dev(y, "y", out_dtype, (shape.R, shape.N))
-        workspace = _workspace(workspace, _sized(lib.moe_grouped_gemm_workspace_size,
-                                                 ctypes.byref(shape)), x.device)
-        _same_device(x, offsets, w, w_scale, y, workspace)
-        _check(lib.moe_grouped_gemm(ctypes.byref(shape), _ptr(x), _ptr(offsets), _ptr(w), _ptr(w_scale),
-                                    _ptr(y), _ptr(workspace), workspace.numel(), _stream(x.device)))
+    if y is None:
+        y = torch.empty((shape.R, shape.N), dtype=out_dtype, device=x.device)
+    _dev(y, "y", out_dtype, (shape.R, shape.N))
+    workspace = _workspace(workspace, x.device, lib.moe_grouped_gemm_workspace_size, ctypes.byref(shape))
+    _same_device(x, offsets, w, w_scale, y, workspace)
+    _run(x.device, lib.moe_grouped_gemm, ctypes.byref(shape), _ptr(x), _ptr(offsets), _ptr(w), _ptr(w_scale),
+         _ptr(y), _ptr(workspace), workspace.numel())
     return y
 
 
@@ -632,13 +642,12 @@ def moe_grouped_gemm_wgrad(dy, x, offsets, *, dw=None):
         raise ValueError("dy must be [R, N], x [R, K] and offsets [G + 1]")
     shape = GemmShape(x.shape[0], offsets.shape[0] - 1, dy.shape[1], x.shape[1], WEIGHTS_BF16, LAYOUT_NK,
                       DTYPE_F32)
-    with torch.cuda.device(x.device):
-        if dw is None:
-            dw = torch.empty((max(shape.G, 0), shape.N, shape.K), dtype=torch.float32, device=x.device)
-        _dev(dw, "dw", torch.float32, (shape.G, shape.N, shape.K))
-        _same_device(x, dy, offsets, dw)
-        _check(load_library().moe_grouped_gemm_wgrad(ctypes.byref(shape), _ptr(dy), _ptr(x), _ptr(offsets),
-                                                     _ptr(dw), _stream(x.device)))
+    if dw is None:
+        dw = torch.empty((max(shape.G, 0), shape.N, shape.K), dtype=torch.float32, device=x.device)
+    _dev(dw, "dw", torch.float32, (shape.G, shape.N, shape.K))
+    _same_device(x, dy, offsets, dw)
+    _run(x.device, load_library().moe_grouped_gemm_wgrad, ctypes.byref(shape), _ptr(dy), _ptr(x), _ptr(offsets),
+         _ptr(dw))
     return dw
 
 
@@ -687,16 +696,15 @@ def moe_lora_forward(x, w, lora_a, lora_b, adapter, scale=None, *, out_dtype=Non
         out_dtype = torch.bfloat16 if y is None else y.dtype
     shape, t = _check_lora(x, w, lora_a, lora_b, adapter, scale, out_dtype)
     lib = load_library()
-    with torch.cuda.device(x.device):
-        if y is None:
-            y = torch.empty((shape.T, shape.N), dtype=out_dtype, device=x.device)
-        _dev(y, "y", out_dtype, (shape.T, shape.N))
-        if xa is not None:
-            _dev(xa, "xa", torch.float32, (shape.T, shape.r))
-        workspace = _workspace(workspace, _sized(lib.moe_lora_workspace_size, ctypes.byref(shape)), x.device)
-        _same_device(x, y, xa, workspace)
-        _check(lib.moe_lora_forward(ctypes.byref(shape), ctypes.byref(t), _ptr(y), _ptr(xa),
-                                    _ptr(workspace), workspace.numel(), _stream(x.device)))
+    if y is None:
+        y = torch.empty((shape.T, shape.N), dtype=out_dtype, device=x.device)
+    _dev(y, "y", out_dtype, (shape.T, shape.N))
+    if xa is not None:
+        _dev(xa, "xa", torch.float32, (shape.T, shape.r))
+    workspace = _workspace(workspace, x.device, lib.moe_lora_workspace_size, ctypes.byref(shape))
+    _same_device(x, y, xa, workspace)
+    _run(x.device, lib.moe_lora_forward, ctypes.byref(shape), ctypes.byref(t), _ptr(y), _ptr(xa),
+         _ptr(workspace), workspace.numel())
     return y
 
 
@@ -713,20 +721,17 @@ def moe_lora_backward(x, w, lora_a, lora_b, adapter, dy, xa, scale=None, *, out_
     _dev(dy, "dy", torch.bfloat16, (shape.T, shape.N))
     _dev(xa, "xa", torch.float32, (shape.T, shape.r))
     lib = load_library()
-    with torch.cuda.device(x.device):
-        for name, dtype, size in (("dx", out_dtype, (shape.T, shape.D)),
-                                  ("da", torch.float32, (shape.L, shape.r, shape.D)),
-                                  ("db", torch.float32, (shape.L, shape.N, shape.r))):
-            if name not in out:
-                out[name] = torch.empty(size, dtype=dtype, device=x.device)
-            _dev(out[name], name, dtype, size)
-        workspace = _workspace(workspace, _sized(lib.moe_lora_backward_workspace_size, ctypes.byref(shape)),
-                               x.device)
-        _same_device(x, dy, xa, out["dx"], out["da"], out["db"], workspace)
-        g = LoraGrads(_ptr(out["dx"]), _ptr(out["da"]), _ptr(out["db"]))
-        _check(lib.moe_lora_backward(ctypes.byref(shape), ctypes.byref(t), _ptr(dy), _ptr(xa),
-                                     ctypes.byref(g), _ptr(workspace), workspace.numel(),
-                                     _stream(x.device)))
+    for name, dtype, size in (("dx", out_dtype, (shape.T, shape.D)),
+                              ("da", torch.float32, (shape.L, shape.r, shape.D)),
+                              ("db", torch.float32, (shape.L, shape.N, shape.r))):
+        if name not in out:
+            out[name] = torch.empty(size, dtype=dtype, device=x.device)
+        _dev(out[name], name, dtype, size)
+    workspace = _workspace(workspace, x.device, lib.moe_lora_backward_workspace_size, ctypes.byref(shape))
+    _same_device(x, dy, xa, out["dx"], out["da"], out["db"], workspace)
+    g = LoraGrads(_ptr(out["dx"]), _ptr(out["da"]), _ptr(out["db"]))
+    _run(x.device, lib.moe_lora_backward, ctypes.byref(shape), ctypes.byref(t), _ptr(dy), _ptr(xa),
+         ctypes.byref(g), _ptr(workspace), workspace.numel())
     return out
 
 
@@ -744,16 +749,16 @@ def moe_orthogonalize(g, *, steps=5, eps=1e-7, out=None, workspace=None):
     if g is None or g.dtype not in _DTYPES:
         raise ValueError("g must be fp32 or bf16")
     _dev(g, "g", g.dtype)
-    nbytes = moe_orthogonalize_workspace_size(g)
-    with torch.cuda.device(g.device):
-        if out is None:
-            out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
-        _dev(out, "out", torch.bfloat16, tuple(g.shape))
-        workspace = _workspace(workspace, nbytes, g.device)
-        _same_device(g, out, workspace)
-        _check(load_library().moe_orthogonalize(*g.shape, _ptr(g), _DTYPES[g.dtype], int(steps), float(eps),
-                                                _ptr(out), _ptr(workspace), workspace.numel(),
-                                                _stream(g.device)))
+    if g.dim() != 3:
+        raise ValueError("g must be [E, M, N]")
+    lib = load_library()
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    _dev(out, "out", torch.bfloat16, tuple(g.shape))
+    workspace = _workspace(workspace, g.device, lib.moe_orthogonalize_workspace_size, *g.shape)
+    _same_device(g, out, workspace)
+    _run(g.device, lib.moe_orthogonalize, *g.shape, _ptr(g), _DTYPES[g.dtype], int(steps), float(eps),
+         _ptr(out), _ptr(workspace), workspace.numel())
     return out
 
 

@@ -13,17 +13,17 @@ namespace {
 template <int RB, bool KMAJ>
 __global__ __launch_bounds__(256) void moe_lora_shrink_kernel(LoraCall c, ShrinkOut o) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  lora_shrink_tile<RB, KMAJ>(c, o, blockIdx.x, 0, 1, lds);
+  lora_shrink_tile<RB, KMAJ>(c, o, blockIdx.x, 0, 0, 1, lds);
 }
 
 template <int RB, bool KMAJ>
 hipError_t launch_shrink(const LoraCall& c, const ShrinkOut& o, hipStream_t s) {
   static std::atomic<uint64_t> done;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(moe_lora_shrink_kernel<RB, KMAJ>),
-                                 shrink_lds_bytes<RB>(kLoraMaxRank, KMAJ), done);
+                                 shrink_lds_bytes<RB>(), done);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((moe_lora_shrink_kernel<RB, KMAJ>), dim3((unsigned)((c.T + 15) / 16)), dim3(256),
-                     shrink_lds_bytes<RB>(c.r, KMAJ), s, c, o);
+                     shrink_lds_bytes<RB>(), s, c, o);
   return hipGetLastError();
 }
 

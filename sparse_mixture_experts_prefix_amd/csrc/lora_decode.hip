@@ -55,13 +55,15 @@ __device__ __forceinline__ int decode_valid(const LoraParts&, const DecodeRows& 
   return r.valid;
 }
 
-// Blocks 0 .. first_block - 1 compute the first product, one per tile of 16
-// rows and slot of 16 (the tile's distinct adapters); the others the projection.
-template <int MT, int RB, bool KMAJ>
+// Blocks 0 .. first_block - 1 compute the first product, one per block of 16 ranks,
+// tile of 16 rows and slot of 16 (the tile's distinct adapters); the others the
+// projection.
+template <int MT, bool KMAJ>
 __global__ __launch_bounds__(256) void moe_lora_decode_kernel(LoraParts p, LoraCall c, ShrinkOut o) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   if (blockIdx.x < p.first_block) {
-    lora_shrink_tile<RB, KMAJ>(c, o, blockIdx.x / 16, blockIdx.x % 16, 16, lds);
+    const int tiles = (c.T + 15) / 16, b = blockIdx.x / 16;
+    lora_shrink_tile<1, KMAJ>(c, o, b % tiles, b / tiles, blockIdx.x % 16, 16, lds);
     return;
   }
   decode_tile_staged<MT, KMAJ, false>(p, lds);
@@ -77,6 +79,7 @@ __global__ __launch_bounds__(256) void moe_lora_finish_kernel(LoraCall c, const 
   if (n >= c.N) return;
   const int l = lora_id(c, t);
   float s = 0.f;
+#pragma unroll 4
   for (int q = 0; q < parts; ++q) s += partial[((int64_t)q * c.T + t) * c.N + n];
   if (l >= 0) {
     const float* v = sv + (int64_t)t * c.r;  // uniform: scalar loads
@@ -87,7 +90,7 @@ __global__ __launch_bounds__(256) void moe_lora_finish_kernel(LoraCall c, const 
       for (int j = 0; j < c.r; ++j) e = fmaf(v[j], bf16_to_f32(m[(int64_t)j * c.N]), e);
     } else {
       const u32x4* m = reinterpret_cast<const u32x4*>(c.expand + ((int64_t)l * c.N + n) * c.r);
-#pragma unroll 2
+#pragma unroll 8
       for (int j = 0; j < c.r / 8; ++j) {
         const u32x4 b = m[j];
 #pragma unroll
@@ -106,31 +109,20 @@ __global__ __launch_bounds__(256) void moe_lora_finish_kernel(LoraCall c, const 
     static_cast<float*>(c.out)[at] = s;
 }
 
-template <int MT, int RB, bool KMAJ>
-hipError_t launch(const LoraCall& c, LoraParts p, const ShrinkOut& o, hipStream_t s) {
+template <int MT, bool KMAJ>
+hipError_t launch(const LoraCall& c, const LoraParts& p, const ShrinkOut& o, hipStream_t s) {
   static std::atomic<uint64_t> done;
-  const int shrink = shrink_lds_bytes<RB>(kLoraMaxRank, KMAJ), gemm = km_lds_bytes<MT>();
-  const int most = shrink > gemm ? shrink : gemm;
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(moe_lora_decode_kernel<MT, RB, KMAJ>), most, done);
+  constexpr int lds = km_lds_bytes<MT>() > shrink_lds_bytes<1>() ? km_lds_bytes<MT>() : shrink_lds_bytes<1>();
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(moe_lora_decode_kernel<MT, KMAJ>), lds, done);
   if (e != hipSuccess) return e;
-  const int need = shrink_lds_bytes<RB>(c.r, KMAJ);
   const int64_t blocks = p.first_block + p.parts * p.n_tiles_n;
-  hipLaunchKernelGGL((moe_lora_decode_kernel<MT, RB, KMAJ>), dim3((unsigned)blocks), dim3(256),
-                     need > gemm ? need : gemm, s, p, c, o);
+  hipLaunchKernelGGL((moe_lora_decode_kernel<MT, KMAJ>), dim3((unsigned)blocks), dim3(256), lds, s, p, c, o);
   return hipGetLastError();
 }
 
-template <int MT, int RB>
-hipError_t launch_layout(const LoraCall& c, bool kmajor, const LoraParts& p, const ShrinkOut& o, hipStream_t s) {
-  return kmajor ? launch<MT, RB, true>(c, p, o, s) : launch<MT, RB, false>(c, p, o, s);
-}
-
 template <int MT>
-hipError_t launch_rank(const LoraCall& c, bool kmajor, const LoraParts& p, const ShrinkOut& o, hipStream_t s) {
-  if (c.r <= 16) return launch_layout<MT, 1>(c, kmajor, p, o, s);
-  if (c.r <= 32) return launch_layout<MT, 2>(c, kmajor, p, o, s);
-  if (c.r <= 64) return launch_layout<MT, 4>(c, kmajor, p, o, s);
-  return launch_layout<MT, 8>(c, kmajor, p, o, s);
+hipError_t launch_layout(const LoraCall& c, bool kmajor, const LoraParts& p, const ShrinkOut& o, hipStream_t s) {
+  return kmajor ? launch<MT, true>(c, p, o, s) : launch<MT, false>(c, p, o, s);
 }
 
 }  // namespace
@@ -148,15 +140,15 @@ hipError_t launch_lora_decode(const LoraCall& c, bool kmajor, float* v, float* s
   p.n_tiles_n = (c.N + 63) / 64;
   p.T = c.T;
   p.parts = parts;
-  p.first_block = (c.T + 15) / 16 * 16;
+  p.first_block = (c.T + 15) / 16 * ((c.r + 15) / 16) * 16;
   const ShrinkOut o{v, sv, parts16};
   hipError_t e;
   if (c.T <= 16)
-    e = launch_rank<1>(c, kmajor, p, o, s);
+    e = launch_layout<1>(c, kmajor, p, o, s);
   else if (c.T <= 32)
-    e = launch_rank<2>(c, kmajor, p, o, s);
+    e = launch_layout<2>(c, kmajor, p, o, s);
   else
-    e = launch_rank<4>(c, kmajor, p, o, s);
+    e = launch_layout<4>(c, kmajor, p, o, s);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((c.N + 255) / 256), (unsigned)c.T);
   if (kmajor)

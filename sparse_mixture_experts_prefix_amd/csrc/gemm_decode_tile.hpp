@@ -40,7 +40,6 @@ __device__ __forceinline__ bf16x8 e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
 struct DecodeRows {
   int g, valid;
   int64_t row0;
-  int part = 0;  // part of K (P::kParts)
 };
 template <int BMD>
 __device__ __forceinline__ bool decode_rows(const GroupedGemm& p, int64_t m, DecodeRows& r) {
@@ -59,8 +58,8 @@ __device__ __forceinline__ int decode_valid(const GroupedGemm& p, const DecodeRo
 // matching up columns; H = bf16(SiLU(g) u), and g | u of the valid rows when
 // kept for the backward pass.  Down: fp32 rows.
 template <bool GATE_UP, int MT, int NG, class P>
-__device__ __forceinline__ void store_tile(const P& p, const f32x4 (&acc)[MT][NG], const DecodeRows& dr,
-                                           int64_t row0, int n0, int N, int valid_rows, int c, int gq) {
+__device__ __forceinline__ void store_tile(const P& p, const f32x4 (&acc)[MT][NG], int64_t row0,
+                                           int n0, int N, int valid_rows, int c, int gq) {
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
 #pragma unroll
@@ -87,7 +86,7 @@ __device__ __forceinline__ void store_tile(const P& p, const f32x4 (&acc)[MT][NG
       } else {
         // padded groups store their padding rows too, ragged ones must not
         if (P::kRagged && i * 16 + 4 * gq + r >= valid_rows) continue;
-        if constexpr (P::kRagged && !P::kParts) {
+        if constexpr (P::kRagged) {
           if (p.out16) {
             bf16_t* Y16 = reinterpret_cast<bf16_t*>(p.C);
 #pragma unroll
@@ -98,11 +97,7 @@ __device__ __forceinline__ void store_tile(const P& p, const f32x4 (&acc)[MT][NG
             continue;
           }
         }
-        float* Y;
-        if constexpr (P::kParts)
-          Y = p.part_out(dr);
-        else
-          Y = reinterpret_cast<float*>(p.C);
+        float* Y = reinterpret_cast<float*>(p.C);
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
           const int n = n0 + j * 16 + c;
@@ -305,7 +300,7 @@ __device__ __forceinline__ void decode_tile(const P& p) {
     }
   }
 
-  store_tile<GATE_UP, MT, NG>(p, acc, dr, row0, n0, N, valid_rows, c, gq);
+  store_tile<GATE_UP, MT, NG>(p, acc, row0, n0, N, valid_rows, c, gq);
 }
 
 // 16-row column groups per tile (gate/up: half gate, half up), waves splitting
@@ -349,9 +344,8 @@ template <int MT> constexpr int km_a_bytes() { return 16 * MT * 128; }
 template <int MT, int NG = 4> constexpr int km_stage_bytes() { return km_a_bytes<MT>() + NG * 2048; }
 // stages per wave: 16-row tiles take two, so two workgroups share a CU (80 KB
 // each) and one's start and end overlap the other's streaming; 32-row tiles
-// take three (144 KB, one workgroup per CU), 48- and 64-row tiles (of the
-// adapters' few-row path) two (112 and 128 KB)
-template <int MT> constexpr int km_stages() { return MT == 2 ? 3 : 2; }
+// take three (144 KB, one workgroup per CU)
+template <int MT> constexpr int km_stages() { return MT == 1 ? 2 : 3; }
 template <int MT, int NG = 4> constexpr int km_lds_bytes() {
   return kKw * km_stages<MT>() * km_stage_bytes<MT, NG>();
 }
@@ -388,8 +382,7 @@ __device__ __forceinline__ void decode_tile_staged(const P& p, char* lds) {
   constexpr int NA = AB / 1024, NB = NG * 2, V = NA + NB;  // 1-KB loads per chunk
   constexpr int HR = 8 * NG;  // gate/up: weight rows of each half of the tile
 
-  int64_t bid = blockIdx.x;
-  if constexpr (P::kParts) bid -= p.first_block;
+  const int64_t bid = blockIdx.x;
   const int64_t n_tile = bid % p.n_tiles_n;
   const int64_t m_tile = bid / p.n_tiles_n;
   DecodeRows dr;
@@ -475,13 +468,11 @@ __device__ __forceinline__ void decode_tile_staged(const P& p, char* lds) {
     for (int j = 0; j < NG; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // this wave's chunks: q = wave + kKw m, m = 0 .. nm - 1
-  // (P::kParts: those of this workgroup's part of K only)
-  int q0 = 0, nq = (K + 63) / 64;
-  if constexpr (P::kParts) p.k_range(dr, q0, nq);
+  const int nq = (K + 63) / 64;
   const int nm = wave < nq ? (nq - 1 - wave) / kKw + 1 : 0;
   char* ring = lds + wave * (S * SB);
   auto issue = [&](int m, int slot) {
-    const int k0 = (q0 + wave + kKw * m) * 64;
+    const int k0 = (wave + kKw * m) * 64;
     char* st = ring + slot * SB;
 #pragma unroll
     for (int b = 0; b < NA; ++b)
@@ -566,7 +557,7 @@ __device__ __forceinline__ void decode_tile_staged(const P& p, char* lds) {
 #pragma unroll
       for (int j = 0; j < NG; ++j) acc[i][j] += red[((w * MT + i) * NG + j) * 64 + lane];
 
-  store_tile<GATE_UP, MT, NG>(p, acc, dr, row0, n0, N, valid_rows, c, gq);
+  store_tile<GATE_UP, MT, NG>(p, acc, row0, n0, N, valid_rows, c, gq);
 }
 
 }  // namespace

@@ -49,7 +49,6 @@ struct GroupedGemm {
   static constexpr bool kRagged = false;  // groups are padded to BM rows
   static constexpr bool kFold = true;     // short last m-tiles fold into the one before
   static constexpr bool kLora = false;    // no adapters beside the product
-  static constexpr bool kParts = false;   // few-row tiles: a workgroup takes all of K
   const uint16_t* A;          // gate/up: x [T, D] (rows gathered by row_token); down: H
   const int32_t* row_token;   // gate/up only
   int64_t lda;                // elements

@@ -3,6 +3,7 @@
 // and the sequence of launches.
 #include "launch.hpp"
 #include "lora.hpp"
+#include "lora_rows.hpp"
 #include "lora_shrink.hpp"
 #include "ops_launch.hpp"
 #include "ragged.hpp"
@@ -10,38 +11,34 @@
 namespace moe {
 namespace {
 
+// Workgroups: the rows' lists (one per adapter, when asked for), then the tiles.
 template <int RB, bool KMAJ>
-__global__ __launch_bounds__(256) void moe_lora_shrink_kernel(LoraCall c, ShrinkOut o) {
+__global__ __launch_bounds__(256) void moe_lora_shrink_kernel(LoraCall c, ShrinkOut o, LoraLists rows) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  lora_shrink_tile<RB, KMAJ>(c, o, blockIdx.x, 0, 0, 1, lds);
+  const int lists = rows.counts ? c.L : 0;
+  if ((int)blockIdx.x < lists)
+    lora_list(c, rows, blockIdx.x, reinterpret_cast<int*>(lds));
+  else
+    lora_shrink_tile<RB, KMAJ>(c, o, blockIdx.x - lists, 0, 0, 1, lds);
 }
 
 template <int RB, bool KMAJ>
-hipError_t launch_shrink(const LoraCall& c, const ShrinkOut& o, hipStream_t s) {
+hipError_t launch_shrink(const LoraCall& c, const ShrinkOut& o, const LoraLists& rows, hipStream_t s) {
   static std::atomic<uint64_t> done;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(moe_lora_shrink_kernel<RB, KMAJ>),
                                  shrink_lds_bytes<RB>(), done);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_lora_shrink_kernel<RB, KMAJ>), dim3((unsigned)((c.T + 15) / 16)), dim3(256),
-                     shrink_lds_bytes<RB>(), s, c, o);
+  hipLaunchKernelGGL((moe_lora_shrink_kernel<RB, KMAJ>), dim3((unsigned)((c.T + 15) / 16 + (rows.counts ? c.L : 0))),
+                     dim3(256), shrink_lds_bytes<RB>(), s, c, o, rows);
   return hipGetLastError();
 }
 
 template <bool KMAJ>
-hipError_t launch_shrink_rank(const LoraCall& c, const ShrinkOut& o, hipStream_t s) {
-  if (c.r <= 16) return launch_shrink<1, KMAJ>(c, o, s);
-  if (c.r <= 32) return launch_shrink<2, KMAJ>(c, o, s);
-  if (c.r <= 64) return launch_shrink<4, KMAJ>(c, o, s);
-  return launch_shrink<8, KMAJ>(c, o, s);
-}
-
-// parts[t] = the two bf16 parts of v[t] ([T][r] fp32)
-__global__ void moe_lora_parts_kernel(const float* v, uint16_t* parts, int64_t n, int r) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  const int64_t t = i / r;
-  const int j = (int)(i - t * r);
-  split_bf16(v[i], parts[t * 2 * r + j], parts[t * 2 * r + r + j]);
+hipError_t launch_shrink_rank(const LoraCall& c, const ShrinkOut& o, const LoraLists& rows, hipStream_t s) {
+  if (c.r <= 16) return launch_shrink<1, KMAJ>(c, o, rows, s);
+  if (c.r <= 32) return launch_shrink<2, KMAJ>(c, o, rows, s);
+  if (c.r <= 64) return launch_shrink<4, KMAJ>(c, o, rows, s);
+  return launch_shrink<8, KMAJ>(c, o, rows, s);
 }
 
 template <class T>
@@ -57,10 +54,10 @@ hipError_t launch_lora_forward(const moe_lora_shape& s, const LoraPlan& p, const
                    static_cast<const bf16_t*>(t.lora_a), static_cast<const bf16_t*>(t.lora_b), t.adapter,
                    t.scale, s.T, s.D, s.N, s.L, s.r, y, s.out_dtype == MOE_DTYPE_BF16};
   if (p.parts)
-    return launch_lora_decode(c, false, xa, at<float>(ws, p.off_sv), nullptr, at<float>(ws, p.off_partial),
-                              p.parts, st);
+    return launch_lora_decode(c, false, ShrinkOut{xa, at<float>(ws, p.off_sv), nullptr, nullptr, nullptr},
+                              LoraLists{}, at<float>(ws, p.off_partial), p.parts, st);
   uint16_t* parts = at<uint16_t>(ws, p.off_v16);
-  const hipError_t e = launch_shrink_rank<false>(c, ShrinkOut{xa, nullptr, parts}, st);
+  const hipError_t e = launch_shrink_rank<false>(c, ShrinkOut{xa, nullptr, parts, nullptr, nullptr}, LoraLists{}, st);
   if (e != hipSuccess) return e;
   return launch_lora_prefill(c, false, parts, p.split ? at<float>(ws, p.off_partial) : nullptr, st);
 }
@@ -75,29 +72,18 @@ hipError_t launch_lora_backward(const moe_lora_shape& s, const LoraBwdPlan& p,
   uint16_t* u16 = at<uint16_t>(ws, p.off_u16);
   uint16_t* xa16 = at<uint16_t>(ws, p.off_xa16);
   int32_t* q = at<int32_t>(ws, p.off_rows);
-  const int T = s.T, L = s.L;
-  // rows by adapter: counts, offsets, padded offsets, sorted rows (and outputs not used here)
-  int32_t *counts = q, *offsets = q + 257, *padded = q + 514, *n_tiles = q + 771, *sorted = q + 772,
-          *row_of = sorted + T, *row_token = row_of + T, *tile_group = row_token + T;
-  hipError_t e = launch_align(t.adapter, T, 1, L, 0, 1, 0, counts, offsets, padded, sorted, row_of, row_token,
-                              tile_group, n_tiles, st);
-  if (e != hipSuccess) return e;
+  const LoraLists rows{q, q + s.L, q + 2 * s.L};
+  float* partial = at<float>(ws, p.off_partial);
+  hipError_t e;
   if (p.parts) {
-    e = launch_lora_decode(c, true, nullptr, at<float>(ws, p.off_su), u16, at<float>(ws, p.off_partial),
+    e = launch_lora_decode(c, true, ShrinkOut{nullptr, at<float>(ws, p.off_su), u16, xa, xa16}, rows, partial,
                            p.parts, st);
   } else {
-    e = launch_shrink_rank<true>(c, ShrinkOut{nullptr, nullptr, u16}, st);
-    if (e == hipSuccess)
-      e = launch_lora_prefill(c, true, u16, p.split ? at<float>(ws, p.off_partial) : nullptr, st);
+    e = launch_shrink_rank<true>(c, ShrinkOut{nullptr, nullptr, u16, xa, xa16}, rows, st);
+    if (e == hipSuccess) e = launch_lora_prefill(c, true, u16, p.split ? partial : nullptr, st);
   }
   if (e != hipSuccess) return e;
-  const int64_t n = (int64_t)T * s.r;
-  hipLaunchKernelGGL(moe_lora_parts_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, xa, xa16, n,
-                     s.r);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return launch_lora_wgrad(LoraRows{counts, offsets, sorted}, t.x, dy, u16, xa16, t.scale, T, s.D, s.N, L, s.r,
-                           g.da, g.db, st);
+  return launch_lora_wgrad(rows, t.x, dy, u16, xa16, t.scale, s.T, s.D, s.N, s.L, s.r, g.da, g.db, st);
 }
 
 }  // namespace moe

@@ -19,6 +19,20 @@ struct LoraCall {
   int out16;              // out is bf16 (else fp32)
 };
 
+// The rows of each adapter: counts[l] of them from offsets[l] of `sorted` on.
+struct LoraLists {
+  int32_t *counts, *offsets, *sorted;
+};
+
+// Outputs of the first product; each but one may be NULL.
+struct ShrinkOut {
+  float* v;           // fp32 [T][r], unscaled (zero rows without an adapter)
+  float* sv;          // fp32 [T][r], scaled
+  uint16_t* parts;    // bf16 [T][2 r]: scaled, upper parts then lower parts
+  const float* xa;    // fp32 [T][r] in ...
+  uint16_t* xa_parts; // ... and its parts (all rows), written on the way
+};
+
 // the row's adapter, or -1
 __device__ __forceinline__ int lora_id(const LoraCall& c, int64_t t) {
   const int l = c.adapter[t];

@@ -1,12 +1,12 @@
 // The adapters' products for few rows (at most 64): two launches.
 //
 // First, in one launch: the projection's weights are streamed once (tiles of all
-// rows x 64 columns of decode_tile_staged, K cut into parts so that the grid
-// fills the chip, fp32 partial sums), while other workgroups compute the
-// adapters' first product.  Then each output is its partial sums, in part
-// order, plus its row's second product in fp32.  Bound by streaming W (2 N K
-// bytes) and the live adapters.
-#include "gemm_decode_tile.hpp"
+// rows x 64 columns, K cut into parts so that the grid fills the chip, fp32
+// partial sums), while other workgroups compute the adapters' first product
+// (and, for the backward pass, the rows' lists).  Then each output is its
+// partial sums, in part order, plus its row's second product in fp32.  Bound by
+// streaming W (2 N K bytes) and the live adapters.
+#include "lora_rows.hpp"
 #include "lora_shrink.hpp"
 #include "ops_launch.hpp"
 #include "ragged.hpp"
@@ -14,59 +14,144 @@
 namespace moe {
 namespace {
 
-// One part of K of the projection for decode_tile_staged: m-tile index = part.
-struct LoraParts {
-  static constexpr bool kRagged = true, kFold = false, kLora = false, kParts = true;
-  static constexpr const int32_t* row_token = nullptr;
-  static constexpr int64_t a_bytes = 0, ld_gu = 0;
-  static constexpr uint16_t* gu_out = nullptr;
-  static constexpr const void* B_shared = nullptr;
-  static constexpr int N_shared = 0, K_shared = 0, E = 1;
-  const uint16_t* A;
-  int64_t lda;
-  const void* B_routed;
-  int N_routed, K_routed;
-  float* C;  // [parts][T][N]
-  int64_t ldc;
-  int64_t n_tiles_n;
-  int T, parts;
-  int64_t first_block;
-  // 64-wide K chunks of part dr.g_part: first one, and how many
-  __device__ __forceinline__ void k_range(const DecodeRows& r, int& q0, int& nq) const {
-    const int all = nq;
-    q0 = (int)((int64_t)r.part * all / parts);
-    nq = (int)((int64_t)(r.part + 1) * all / parts) - q0;
+// Projection tile: T <= 16 MT rows x 64 columns, chunks q0 .. q1 - 1 of 64 k.  A
+// stage (all rows, 64 columns) is shared by the four waves, 16 columns each, in a
+// ring of four stages: three in flight, one barrier per stage.  40 to 64 KB of LDS
+// per workgroup, so two or more share a CU (each wave with its own ring of whole
+// stages took 128 KB at 64 rows: one workgroup per CU, 24 us against 15 us for
+// 64 rows x 5760 columns x 2880).
+constexpr int kStages = 4;
+// (a multiple of 4 KB: the waves issue equally many 1-KB loads)
+template <int MT> constexpr int tile_stage_bytes() { return (MT * 2048 + 8192 + 4095) / 4096 * 4096; }
+template <int MT> constexpr int tile_lds_bytes() { return kStages * tile_stage_bytes<MT>(); }
+
+__device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
+// K-major weights: 64 k-rows of 64 columns, chunk c (8 columns) of k-row r at c ^ col_swz(r), so
+// that a 32-lane half of a transposing read (k-rows R .. R + 3 and R + 8 .. R + 11,
+// two chunks each) hits every bank once
+__device__ __forceinline__ int col_swz(int r) { return 2 * ((r >> 1) & 1) + 4 * ((r >> 3) & 1); }
+
+template <int MT, bool KMAJ>
+__device__ __forceinline__ void project_tile(const LoraCall& c, int n0, int q0, int q1, float* out, char* lds) {
+  constexpr int SB = tile_stage_bytes<MT>(), AB = MT * 2048;
+  constexpr int LA = MT * 2;            // 1-KB blocks of rows
+  constexpr int V = SB / 4096;          // loads per wave and stage
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, gq = lane >> 4, ir = lane >> 3, ip = lane & 7;
+  const int K = c.K, N = c.N;
+  const __amdgpu_buffer_rsrc_t rsA = lora_rsrc(c.in, (uint32_t)(c.T * K * 2));
+  const __amdgpu_buffer_rsrc_t rsB = lora_rsrc(c.w, (uint32_t)((int64_t)N * K * 2));
+  // block b of a stage: rows 8 b + ir (b < LA), else weight rows (or k-rows) 8 (b - LA) + ir
+  auto issue = [&](int q, int slot) {
+    const int k0 = q * 64;
+    char* st = lds + __builtin_amdgcn_readfirstlane(slot * SB);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int b = wave + 4 * i;  // uniform
+      if (b < LA) {
+        const int r = 8 * b + ir, k = k0 + 8 * (ip ^ row_swz(r));
+        lds_dma16(rsA, st + b * 1024, r < c.T && k < K ? (uint32_t)((r * K + k) * 2) : kShrinkOob, 0);
+      } else if (b < LA + 8) {
+        const int r = 8 * (b - LA) + ir;
+        uint32_t off;
+        if constexpr (KMAJ) {
+          const int k = k0 + r, n = n0 + 8 * (ip ^ col_swz(r));
+          off = k < K && n < N ? (uint32_t)((k * N + n) * 2) : kShrinkOob;
+        } else {
+          const int k = k0 + 8 * (ip ^ row_swz(r)), n = n0 + r;
+          off = k < K && n < N ? (uint32_t)((n * K + k) * 2) : kShrinkOob;
+        }
+        lds_dma16<true>(rsB, st + b * 1024, off, 0);  // read once: non-temporal
+      } else {  // zeros into the stage's unused end: the waves' counts of loads stay equal
+        lds_dma16(rsA, st + b * 1024, kShrinkOob, 0);
+      }
+    }
+  };
+  static_assert(4 * V * 1024 == SB, "a stage is the waves' loads");
+  f32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int n = q1 - q0;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s)
+    if (s < n) issue(q0 + s, s);
+  for (int s = 0; s < n; ++s) {
+    const int later = min(n - 1 - s, kStages - 2);
+    if (later >= 2)
+      shrink_wait<2 * V>();
+    else if (later == 1)
+      shrink_wait<V>();
+    else
+      shrink_wait<0>();
+    __builtin_amdgcn_s_barrier();  // stage s is whole; every wave has read stage s - 1
+    asm volatile("" ::: "memory");
+    if (s + kStages - 1 < n) issue(q0 + s + kStages - 1, (s + kStages - 1) % kStages);
+    const char* st = lds + (s % kStages) * SB;
+    typedef short i16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) i16x4 lds_v4;
+    typedef __attribute__((address_space(3))) char lds_char;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // step h takes k = 32 h + 8 gq + (0 .. 7)
+      bf16x8 b;
+      if constexpr (KMAJ) {
+        const int r = 32 * h + 8 * gq + (col >> 2), ch = 2 * wave + ((col & 3) >> 1);
+        const char* q = st + AB + r * 128 + 16 * (ch ^ col_swz(r)) + 8 * (col & 1);
+        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)((lds_char*)q));
+        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)((lds_char*)(q + 4 * 128)));
+        b = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      } else {
+        const int r = 16 * wave + col;
+        b = *reinterpret_cast<const bf16x8*>(st + AB + r * 128 + 16 * ((4 * h + gq) ^ row_swz(r)));
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int r = 16 * i + col;
+        const bf16x8 a = *reinterpret_cast<const bf16x8*>(st + r * 128 + 16 * ((4 * h + gq) ^ row_swz(r)));
+        acc[i] = mfma16(a, b, acc[i]);
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of stage s are done
   }
-  __device__ __forceinline__ float* part_out(const DecodeRows& r) const {
-    return C + (int64_t)r.part * T * ldc;
-  }
-};
-template <int BMD>
-__device__ __forceinline__ bool decode_rows(const LoraParts& p, int64_t m, DecodeRows& r) {
-  if (m >= p.parts) return false;
-  r.g = 0;
-  r.part = (int)m;
-  r.row0 = 0;
-  r.valid = p.T;
-  return true;
-}
-template <int BMD>
-__device__ __forceinline__ int decode_valid(const LoraParts&, const DecodeRows& r) {
-  return r.valid;
+  // lane (col, gq) holds rows 16 i + 4 gq + r of column n0 + 16 wave + col
+  const int cn = n0 + 16 * wave + col;
+  if (cn >= N) return;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * i + 4 * gq + r;
+      if (t < c.T) out[(int64_t)t * N + cn] = acc[i][r];
+    }
 }
 
-// Blocks 0 .. first_block - 1 compute the first product, one per block of 16 ranks,
-// tile of 16 rows and slot of 16 (the tile's distinct adapters); the others the
-// projection.
+struct FewRows {
+  int shrink, lists;  // workgroups of the first product, and of the rows' lists
+  int tiles, parts;   // column tiles, parts of K
+  float* partial;     // [parts][T][N]
+};
+
+// Workgroups: the first product, one per block of 16 ranks, tile of 16 rows and slot
+// of 16 (the tile's distinct adapters); the rows' lists; the projection.
 template <int MT, bool KMAJ>
-__global__ __launch_bounds__(256) void moe_lora_decode_kernel(LoraParts p, LoraCall c, ShrinkOut o) {
+__global__ __launch_bounds__(256) void moe_lora_decode_kernel(LoraCall c, ShrinkOut o, LoraLists rows, FewRows f) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  if (blockIdx.x < p.first_block) {
-    const int tiles = (c.T + 15) / 16, b = blockIdx.x / 16;
-    lora_shrink_tile<1, KMAJ>(c, o, b % tiles, b / tiles, blockIdx.x % 16, 16, lds);
+  int b = blockIdx.x;
+  if (b < f.shrink) {
+    const int tiles = (c.T + 15) / 16, u = b / 16;
+    lora_shrink_tile<1, KMAJ>(c, o, u % tiles, u / tiles, b % 16, 16, lds);
     return;
   }
-  decode_tile_staged<MT, KMAJ, false>(p, lds);
+  b -= f.shrink;
+  if (b < f.lists) {
+    lora_list(c, rows, b, reinterpret_cast<int*>(lds));
+    return;
+  }
+  b -= f.lists;
+  const int part = b / f.tiles, nq = (c.K + 63) / 64;
+  project_tile<MT, KMAJ>(c, (b % f.tiles) * 64, (int)((int64_t)part * nq / f.parts),
+                         (int)((int64_t)(part + 1) * nq / f.parts),
+                         f.partial + (int64_t)part * c.T * c.N, lds);
 }
 
 // out[t][n] = sum of the parts (in part order) + sum_j sv[t][j] expand[a][n][j]
@@ -110,51 +195,34 @@ __global__ __launch_bounds__(256) void moe_lora_finish_kernel(LoraCall c, const 
 }
 
 template <int MT, bool KMAJ>
-hipError_t launch(const LoraCall& c, const LoraParts& p, const ShrinkOut& o, hipStream_t s) {
+hipError_t launch(const LoraCall& c, const ShrinkOut& o, const LoraLists& rows, const FewRows& f, hipStream_t s) {
   static std::atomic<uint64_t> done;
-  constexpr int lds = km_lds_bytes<MT>() > shrink_lds_bytes<1>() ? km_lds_bytes<MT>() : shrink_lds_bytes<1>();
+  constexpr int lds = tile_lds_bytes<MT>() > shrink_lds_bytes<1>() ? tile_lds_bytes<MT>() : shrink_lds_bytes<1>();
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(moe_lora_decode_kernel<MT, KMAJ>), lds, done);
   if (e != hipSuccess) return e;
-  const int64_t blocks = p.first_block + p.parts * p.n_tiles_n;
-  hipLaunchKernelGGL((moe_lora_decode_kernel<MT, KMAJ>), dim3((unsigned)blocks), dim3(256), lds, s, p, c, o);
+  const int64_t blocks = f.shrink + f.lists + (int64_t)f.tiles * f.parts;
+  hipLaunchKernelGGL((moe_lora_decode_kernel<MT, KMAJ>), dim3((unsigned)blocks), dim3(256), lds, s, c, o, rows, f);
   return hipGetLastError();
-}
-
-template <int MT>
-hipError_t launch_layout(const LoraCall& c, bool kmajor, const LoraParts& p, const ShrinkOut& o, hipStream_t s) {
-  return kmajor ? launch<MT, true>(c, p, o, s) : launch<MT, false>(c, p, o, s);
 }
 
 }  // namespace
 
-hipError_t launch_lora_decode(const LoraCall& c, bool kmajor, float* v, float* sv, uint16_t* parts16,
+hipError_t launch_lora_decode(const LoraCall& c, bool kmajor, const ShrinkOut& o, const LoraLists& rows,
                               float* partial, int parts, hipStream_t s) {
-  LoraParts p{};
-  p.A = c.in;
-  p.lda = c.K;
-  p.B_routed = c.w;
-  p.N_routed = c.N;
-  p.K_routed = c.K;
-  p.C = partial;
-  p.ldc = c.N;
-  p.n_tiles_n = (c.N + 63) / 64;
-  p.T = c.T;
-  p.parts = parts;
-  p.first_block = (c.T + 15) / 16 * ((c.r + 15) / 16) * 16;
-  const ShrinkOut o{v, sv, parts16};
+  const FewRows f{(c.T + 15) / 16 * ((c.r + 15) / 16) * 16, rows.counts ? c.L : 0, (c.N + 63) / 64, parts, partial};
   hipError_t e;
   if (c.T <= 16)
-    e = launch_layout<1>(c, kmajor, p, o, s);
+    e = kmajor ? launch<1, true>(c, o, rows, f, s) : launch<1, false>(c, o, rows, f, s);
   else if (c.T <= 32)
-    e = launch_layout<2>(c, kmajor, p, o, s);
+    e = kmajor ? launch<2, true>(c, o, rows, f, s) : launch<2, false>(c, o, rows, f, s);
   else
-    e = launch_layout<4>(c, kmajor, p, o, s);
+    e = kmajor ? launch<4, true>(c, o, rows, f, s) : launch<4, false>(c, o, rows, f, s);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((c.N + 255) / 256), (unsigned)c.T);
   if (kmajor)
-    hipLaunchKernelGGL(moe_lora_finish_kernel<true>, grid, dim3(256), 0, s, c, partial, parts, sv);
+    hipLaunchKernelGGL(moe_lora_finish_kernel<true>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
   else
-    hipLaunchKernelGGL(moe_lora_finish_kernel<false>, grid, dim3(256), 0, s, c, partial, parts, sv);
+    hipLaunchKernelGGL(moe_lora_finish_kernel<false>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
   return hipGetLastError();
 }
 

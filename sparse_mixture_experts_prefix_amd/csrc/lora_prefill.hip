@@ -12,7 +12,7 @@ namespace {
 
 // One dense group of T rows for prefill_tile (field names as GroupedGemm's).
 struct LoraGemm {
-  static constexpr bool kRagged = true, kFold = false, kLora = true, kParts = false;
+  static constexpr bool kRagged = true, kFold = false, kLora = true;
   static constexpr const int32_t* row_token = nullptr;
   static constexpr int64_t a_bytes = 0, ld_gu = 0;
   static constexpr uint16_t* gu_out = nullptr;

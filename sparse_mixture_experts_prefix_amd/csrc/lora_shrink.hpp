@@ -19,12 +19,6 @@
 namespace moe {
 namespace {
 
-struct ShrinkOut {
-  float* v;        // fp32 [T][r], unscaled (zero rows without an adapter), or NULL
-  float* sv;       // fp32 [T][r], scaled, or NULL
-  uint16_t* parts; // bf16 [T][2 r]: scaled, upper parts then lower parts, or NULL
-};
-
 constexpr uint32_t kShrinkOob = 0x80000000u;
 constexpr int kShrinkWaves = 4;
 
@@ -59,6 +53,13 @@ __device__ __forceinline__ void lora_shrink_tile(const LoraCall& c, const Shrink
   if (slot == 0 && rb == 0 && o.v) {  // rows without an adapter
     for (int e = threadIdx.x; e < rows * c.r; e += blockDim.x)
       if (lora_id(c, t0 + e / c.r) < 0) o.v[t0 * c.r + e] = 0.f;
+  }
+  if (slot == 0 && rb == 0 && o.xa) {
+    for (int e = threadIdx.x; e < rows * c.r; e += blockDim.x) {
+      const int64_t t = t0 + e / c.r;
+      const int j = e % c.r;
+      split_bf16(o.xa[t * c.r + j], o.xa_parts[t * 2 * c.r + j], o.xa_parts[t * 2 * c.r + c.r + j]);
+    }
   }
   // distinct adapters: bit `row` of `left` is a row whose adapter is yet to come
   uint32_t left = (uint32_t)__ballot(lane < 16 && my >= 0);

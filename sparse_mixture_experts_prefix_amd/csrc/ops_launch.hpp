@@ -27,14 +27,11 @@ hipError_t launch_lora_backward(const moe_lora_shape& s, const LoraBwdPlan& p,
 // bf16 parts; partial (or NULL: no cut along K) room for partial tiles.
 hipError_t launch_lora_prefill(const LoraCall& c, bool kmajor, const uint16_t* parts16, float* partial,
                                hipStream_t s);
-// At most 64 rows, both products: v (or NULL), sv and parts16 (or NULL) as
-// ShrinkOut; partial [parts][T][N].
-hipError_t launch_lora_decode(const LoraCall& c, bool kmajor, float* v, float* sv, uint16_t* parts16,
+// At most 64 rows, both products (o.sv is needed); rows.counts set: the rows' lists
+// too.  partial: fp32 [parts][T][N].
+hipError_t launch_lora_decode(const LoraCall& c, bool kmajor, const ShrinkOut& o, const LoraLists& rows,
                               float* partial, int parts, hipStream_t s);
-struct LoraRows {
-  const int32_t *counts, *offsets, *sorted;  // rows by adapter (align's outputs)
-};
-hipError_t launch_lora_wgrad(const LoraRows& rows, const void* x, const void* dy, const uint16_t* u,
+hipError_t launch_lora_wgrad(const LoraLists& rows, const void* x, const void* dy, const uint16_t* u,
                              const uint16_t* xa, const float* scale, int T, int D, int N, int L, int r,
                              float* da, float* db, hipStream_t s);
 hipError_t launch_orthogonalize(int E, int M, int N, const OrthPlan& p, const void* g, int g_dtype,

@@ -139,7 +139,7 @@ int make_lora_backward_plan(const moe_lora_shape* s, LoraBwdPlan* p) {
   p->off_su = l.take(few ? sizeof(float) * T * r : 0);
   p->off_u16 = l.take(sizeof(uint16_t) * T * 2 * r);
   p->off_xa16 = l.take(sizeof(uint16_t) * T * 2 * r);
-  p->off_rows = l.take(sizeof(int32_t) * (772 + 4 * T + 1));
+  p->off_rows = l.take(sizeof(int32_t) * (2 * s->L + T));
   p->off_partial = l.take(few ? sizeof(float) * p->parts * T * s->D : p->split ? kPartialBytes : 0);
   p->total = l.o;
   return MOE_OK;

@@ -45,7 +45,7 @@ struct LoraBwdPlan {
   size_t off_su;       // few rows: fp32 [T][r], u
   size_t off_u16;      // bf16 [T][2 r]: u's two parts
   size_t off_xa16;     // bf16 [T][2 r]: xa's
-  size_t off_rows;     // int32 [772 + 4 T + 1]: rows by adapter (see launch_lora_backward)
+  size_t off_rows;     // int32 [2 L + T]: the adapters' rows (LoraLists)
   size_t off_partial;  // fp32 [parts][T][D], or partial tiles
   size_t total;
 };

@@ -21,7 +21,7 @@ __device__ __forceinline__ int ragged_rows(const int32_t* offsets, int g, int R)
 // C = A W[g]^T (or A W[g], K-major) over the groups' rows, for prefill_tile,
 // decode_tile and decode_tile_staged (field names as GroupedGemm's).
 struct RaggedGemm {
-  static constexpr bool kRagged = true, kFold = true, kLora = false, kParts = false;
+  static constexpr bool kRagged = true, kFold = true, kLora = false;
   static constexpr const int32_t* row_token = nullptr;  // rows are not gathered
   static constexpr int64_t a_bytes = 0, ld_gu = 0;
   static constexpr uint16_t* gu_out = nullptr;

@@ -168,21 +168,22 @@ __device__ __forceinline__ bool orth_tile(const OrthProduct& p, int64_t b, OrthT
   return true;
 }
 
-// Eight results v of row `row`, columns col .. col + 7: all of a result's reads
-// and writes are 16 bytes wide.
-__device__ __forceinline__ void emit_row(const OrthProduct& p, int64_t at, int row, int col, float (&v)[8]) {
-  const int64_t i = at + (int64_t)row * p.N + col;
+// The addends of eight results (c0 and c1 at element i), and the results: all
+// reads and writes are 16 bytes wide.
+struct Addend {
+  f16x8 h, l;
+};
+__device__ __forceinline__ Addend load_addend(const OrthProduct& p, int64_t i, bool in) {
+  Addend a;
 #pragma unroll
-  for (int u = 0; u < 8; ++u) v[u] *= p.alpha;
-  if (p.c0) {
-    const f16x8 h = *reinterpret_cast<const f16x8*>(p.c0 + i);
-    f16x8 l;
+  for (int u = 0; u < 8; ++u) a.h[u] = a.l[u] = (f16)0.f;
+  if (in && p.c0) a.h = *reinterpret_cast<const f16x8*>(p.c0 + i);
+  if (in && p.c1) a.l = *reinterpret_cast<const f16x8*>(p.c1 + i);
+  return a;
+}
+__device__ __forceinline__ void emit8(const OrthProduct& p, int64_t i, const Addend& a, float (&v)[8]) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) l[u] = (f16)0.f;
-    if (p.c1) l = *reinterpret_cast<const f16x8*>(p.c1 + i);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = fmaf(p.beta, (float)h[u] + (float)l[u], v[u]);
-  }
+  for (int u = 0; u < 8; ++u) v[u] = fmaf(p.beta, (float)a.h[u] + (float)a.l[u], v[u] * p.alpha);
   if (p.out) {
     u32x4 w;
 #pragma unroll
@@ -203,31 +204,55 @@ __device__ __forceinline__ void emit_row(const OrthProduct& p, int64_t at, int r
 
 // A tile of ROWS x TS results in LDS (fp32, rows of TS + 8 so that the lanes' column
 // and row accesses spread over the banks) at rows m, columns n of the result:
-// stored row by row, and (mirror) column by column as rows of the transposed place.
-// c0 is symmetric too, so the transposed place's own c0 serves there.
+// stored row by row, and (mirror) column by column as rows of the transposed place
+// (c0 is symmetric too, so the transposed place's own c0 serves there).  Four
+// pieces per thread at a time, their addends' loads together: one after the other
+// each waited out a memory latency (X step of update_square 1.93 ms, then 1.5 ms).
 template <int TS>
 constexpr int tile_pitch() { return TS + 8; }
 template <int ROWS, int TS>
 __device__ __forceinline__ void emit_tile(const OrthProduct& p, int64_t at, int m, int n, const float* tile,
                                           bool mirror) {
   const int rows = min(ROWS, p.M - m), cols = min(TS, p.N - n);  // multiples of 8
-  for (int q = threadIdx.x; q < ROWS * (TS / 8); q += 256) {
-    const int r = q / (TS / 8), c = q % (TS / 8) * 8;
-    if (r >= rows || c >= cols) continue;
-    float v[8];
-    const float4 a = *reinterpret_cast<const float4*>(tile + r * tile_pitch<TS>() + c);
-    const float4 b = *reinterpret_cast<const float4*>(tile + r * tile_pitch<TS>() + c + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    emit_row(p, at, m + r, n + c, v);
+  constexpr int PIECES = ROWS * TS / 8 / 256, U = PIECES < 4 ? PIECES : 4;
+  static_assert(PIECES % U == 0, "whole batches");
+#pragma unroll 1
+  for (int q0 = 0; q0 < PIECES; q0 += U) {
+    Addend a[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int q = (q0 + u) * 256 + threadIdx.x, r = q / (TS / 8), c = q % (TS / 8) * 8;
+      a[u] = load_addend(p, at + (int64_t)(m + r) * p.N + n + c, r < rows && c < cols);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int q = (q0 + u) * 256 + threadIdx.x, r = q / (TS / 8), c = q % (TS / 8) * 8;
+      if (r >= rows || c >= cols) continue;
+      float v[8];
+      const float4 x = *reinterpret_cast<const float4*>(tile + r * tile_pitch<TS>() + c);
+      const float4 y = *reinterpret_cast<const float4*>(tile + r * tile_pitch<TS>() + c + 4);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+      emit8(p, at + (int64_t)(m + r) * p.N + n + c, a[u], v);
+    }
   }
   if (!mirror) return;
-  for (int q = threadIdx.x; q < TS * (ROWS / 8); q += 256) {
-    const int c = q % TS, r = q / TS * 8;
-    if (r >= rows || c >= cols) continue;
-    float v[8];
+#pragma unroll 1
+  for (int q0 = 0; q0 < PIECES; q0 += U) {
+    Addend a[U];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = tile[(r + u) * tile_pitch<TS>() + c];
-    emit_row(p, at, n + c, m + r, v);
+    for (int u = 0; u < U; ++u) {
+      const int q = (q0 + u) * 256 + threadIdx.x, c = q % TS, r = q / TS * 8;
+      a[u] = load_addend(p, at + (int64_t)(n + c) * p.N + m + r, r < rows && c < cols);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int q = (q0 + u) * 256 + threadIdx.x, c = q % TS, r = q / TS * 8;
+      if (r >= rows || c >= cols) continue;
+      float v[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v[w] = tile[(r + w) * tile_pitch<TS>() + c];
+      emit8(p, at + (int64_t)(n + c) * p.N + m + r, a[u], v);
+    }
   }
 }
 

@@ -395,7 +395,7 @@ struct Split {
 };
 
 template <class P>
-__device__ __forceinline__ Split split_of(const P& p, int64_t mt) {
+__host__ __device__ __forceinline__ Split split_of(const P& p, int64_t mt) {
   Split sp;
   sp.V = mt * p.n_tiles_n;
   sp.R = 0;
@@ -907,44 +907,61 @@ __device__ __forceinline__ void prefill_tile(const P& p, char* lds) {
       }
       return;
     }
-    // bf16 rows: stored from registers as pairs of columns, as H above
+    // bf16 rows: stored from registers as pairs of columns, as H above.  Pair q of a
+    // block holds rows 8 (q / 2) + 2 (q % 2) + 4 kh + (0, 1): the even lane takes the
+    // first, the odd lane the second, so the row is a uniform part (in the scalar
+    // offset) and the lane's 4 kh + lane % 2 (in the vector offset, with its columns).
     if constexpr (P::kRagged) {
       if (p.out16) {
-        const int rows = XRT ? BM + extra : valid_rows;
-        const __amdgpu_buffer_rsrc_t rsY =
-            make_rsrc(reinterpret_cast<bf16_t*>(p.C) + row0 * p.ldc, (uint32_t)(rows * p.ldc * 2));
         const bool odd = lane & 1;
-        auto store_pair = [&](float v0, float v1, int row, int col) {
+        const int lrow = 4 * kh + (odd ? 1 : 0);
+        const __amdgpu_buffer_rsrc_t rsY =
+            make_rsrc(reinterpret_cast<bf16_t*>(p.C) + row0 * p.ldc,
+                      (uint32_t)((int64_t)(XRT ? valid_rows + extra : valid_rows) * p.ldc * 2));
+        uint32_t voff[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = n0 + b_row_of<GATE_UP>(wn, j) + (lr & ~1);
+          voff[j] = n < N ? (uint32_t)((lrow * p.ldc + n) * 2) : kOob;
+        }
+        auto store_pair = [&](float v0, float v1, uint32_t vo, uint32_t soff) {
           const float send = odd ? v0 : v1;
           const float got = __builtin_bit_cast(
               float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, send), 0xB1, 0xF, 0xF, false));
           const uint32_t v = (uint32_t)f32_to_bf16(odd ? got : v0) |
                              ((uint32_t)f32_to_bf16(odd ? v1 : got) << 16);
-          const uint32_t off = (row < rows && col < N) ? (uint32_t)((row * p.ldc + col) * 2) : kOob;
-          __builtin_amdgcn_raw_buffer_store_b32(v, rsY, off, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b32(v, rsY, vo, soff, 0);
         };
+        auto store_rows = [&](const bool check) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i >= act) continue;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int r = 2 * q + (odd ? 1 : 0);
-            const int row = a_row(i) + 8 * (r >> 2) + 4 * kh + (r & 3);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              store_pair(acc[i][j][2 * q], acc[i][j][2 * q + 1], row,
-                         n0 + b_row_of<GATE_UP>(wn, j) + (lr & ~1));
-          }
-        }
-        if constexpr (XRT) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int i = 0; i < 4; ++i) {
+            if (i >= act) continue;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-              const int r = 2 * q + (odd ? 1 : 0);
-              store_pair(xr->acc[h][2 * q], xr->acc[h][2 * q + 1], BM + 8 * (r >> 2) + 4 * kh + (r & 3),
-                         n0 + b_row_of<GATE_UP>(wn, xblock<GATE_UP>(wm, h)) + (lr & ~1));
+              const int rb = a_row(i) + 8 * (q >> 1) + 2 * (q & 1);
+              const uint32_t soff = (uint32_t)(rb * p.ldc * 2);
+              const bool ok = !check || rb + lrow < valid_rows;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                store_pair(acc[i][j][2 * q], acc[i][j][2 * q + 1], ok ? voff[j] : kOob, soff);
             }
+          }
+        };
+        if (valid_rows >= BM)
+          store_rows(false);
+        else
+          store_rows(true);
+        if constexpr (XRT) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t vo = wm ? voff[xblock<GATE_UP>(1, h)] : voff[xblock<GATE_UP>(0, h)];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const int rb = BM + 8 * (q >> 1) + 2 * (q & 1);
+              store_pair(xr->acc[h][2 * q], xr->acc[h][2 * q + 1], rb + lrow < BM + extra ? vo : kOob,
+                         (uint32_t)(rb * p.ldc * 2));
+            }
+          }
         }
         return;
       }

@@ -16,14 +16,14 @@ namespace {
 
 // Projection tile: T <= 16 MT rows x 64 columns, chunks q0 .. q1 - 1 of 64 k.  A
 // stage (all rows, 64 columns) is shared by the four waves, 16 columns each, in a
-// ring of four stages: three in flight, one barrier per stage.  40 to 64 KB of LDS
-// per workgroup, so two or more share a CU (each wave with its own ring of whole
+// ring of four (64 rows) or six stages, all but one in flight, one barrier per stage.  64
+// or 72 KB of LDS per workgroup, so two share a CU (each wave with its own ring of whole
 // stages took 128 KB at 64 rows: one workgroup per CU, 24 us against 15 us for
 // 64 rows x 5760 columns x 2880).
-constexpr int kStages = 4;
 // (a multiple of 4 KB: the waves issue equally many 1-KB loads)
 template <int MT> constexpr int tile_stage_bytes() { return (MT * 2048 + 8192 + 4095) / 4096 * 4096; }
-template <int MT> constexpr int tile_lds_bytes() { return kStages * tile_stage_bytes<MT>(); }
+template <int MT> constexpr int tile_stages() { return MT == 4 ? 4 : 6; }
+template <int MT> constexpr int tile_lds_bytes() { return tile_stages<MT>() * tile_stage_bytes<MT>(); }
 
 __device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
 // K-major weights: 64 k-rows of 64 columns, chunk c (8 columns) of k-row r at c ^ col_swz(r), so
@@ -33,7 +33,7 @@ __device__ __forceinline__ int col_swz(int r) { return 2 * ((r >> 1) & 1) + 4 * 
 
 template <int MT, bool KMAJ>
 __device__ __forceinline__ void project_tile(const LoraCall& c, int n0, int q0, int q1, float* out, char* lds) {
-  constexpr int SB = tile_stage_bytes<MT>(), AB = MT * 2048;
+  constexpr int SB = tile_stage_bytes<MT>(), AB = MT * 2048, S = tile_stages<MT>();
   constexpr int LA = MT * 2;            // 1-KB blocks of rows
   constexpr int V = SB / 4096;          // loads per wave and stage
   const int lane = threadIdx.x & 63;
@@ -74,11 +74,15 @@ __device__ __forceinline__ void project_tile(const LoraCall& c, int n0, int q0, 
   for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int n = q1 - q0;
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s)
+  for (int s = 0; s < S - 1; ++s)
     if (s < n) issue(q0 + s, s);
   for (int s = 0; s < n; ++s) {
-    const int later = min(n - 1 - s, kStages - 2);
-    if (later >= 2)
+    const int later = min(n - 1 - s, S - 2);
+    if (S > 5 && later >= 4)
+      shrink_wait<(S > 5 ? 4 : 2) * V>();
+    else if (S > 4 && later == 3)
+      shrink_wait<(S > 4 ? 3 : 2) * V>();
+    else if (later >= 2)
       shrink_wait<2 * V>();
     else if (later == 1)
       shrink_wait<V>();
@@ -86,8 +90,8 @@ __device__ __forceinline__ void project_tile(const LoraCall& c, int n0, int q0, 
       shrink_wait<0>();
     __builtin_amdgcn_s_barrier();  // stage s is whole; every wave has read stage s - 1
     asm volatile("" ::: "memory");
-    if (s + kStages - 1 < n) issue(q0 + s + kStages - 1, (s + kStages - 1) % kStages);
-    const char* st = lds + (s % kStages) * SB;
+    if (s + S - 1 < n) issue(q0 + s + S - 1, (s + S - 1) % S);
+    const char* st = lds + (s % S) * SB;
     typedef short i16x4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) i16x4 lds_v4;
     typedef __attribute__((address_space(3))) char lds_char;
@@ -154,11 +158,64 @@ __global__ __launch_bounds__(256) void moe_lora_decode_kernel(LoraCall c, Shrink
                          f.partial + (int64_t)part * c.T * c.N, lds);
 }
 
-// out[t][n] = sum of the parts (in part order) + sum_j sv[t][j] expand[a][n][j]
-// (K-major: expand[a][j][n]); one row and 256 columns per workgroup
-template <bool KMAJ>
+__device__ __forceinline__ void store_out(const LoraCall& c, int64_t at, float v) {
+  if (c.out16)
+    static_cast<bf16_t*>(c.out)[at] = f32_to_bf16(v);
+  else
+    static_cast<float*>(c.out)[at] = v;
+}
+
+// out[t][n] = sum of the parts (in part order) + sum_j sv[t][j] expand[a][n][j], one
+// row and 256 columns per workgroup.  G lanes share a row of expand (16 bytes each, 8 G >=
+// r), so a wave's loads are one contiguous piece (a row per lane read 16 bytes of 64
+// different lines per load: 11 us against 8 us at 64 rows x 5760 columns, rank 64); the
+// lanes' sums are added in a fixed tree.
+template <int G>
 __global__ __launch_bounds__(256) void moe_lora_finish_kernel(LoraCall c, const float* partial, int parts,
                                                               const float* sv) {
+  __shared__ float es[256];
+  const int t = blockIdx.y, lane = threadIdx.x & 63, w0 = threadIdx.x & ~63;
+  const int n0 = blockIdx.x * 256 + w0;  // first column of this wave
+  const int l = lora_id(c, t);
+  const int n = n0 + lane;
+  float s = 0.f;
+  if (n < c.N) {
+#pragma unroll 4
+    for (int q = 0; q < parts; ++q) s += partial[((int64_t)q * c.T + t) * c.N + n];
+  }
+  if (l >= 0) {  // uniform
+    const int g = lane % G, row = lane / G;
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = 8 * g < c.r ? sv[(int64_t)t * c.r + 8 * g + u] : 0.f;
+    u32x4 b[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int m = n0 + i * (64 / G) + row;
+      b[i] = u32x4{0, 0, 0, 0};
+      if (m < c.N && 8 * g < c.r) b[i] = ld16(c.expand + ((int64_t)l * c.N + m) * c.r + 8 * g);
+    }
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      float e = 0.f;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        e = fmaf(v[2 * h], __builtin_bit_cast(float, b[i][h] << 16), e);
+        e = fmaf(v[2 * h + 1], __builtin_bit_cast(float, b[i][h] & 0xFFFF0000u), e);
+      }
+#pragma unroll
+      for (int off = 1; off < G; off <<= 1) e += __shfl_xor(e, off);
+      if (g == 0) es[w0 + i * (64 / G) + row] = e;
+    }
+    __builtin_amdgcn_wave_barrier();  // the wave's own results, in its own words
+    s += es[threadIdx.x];
+  }
+  if (n < c.N) store_out(c, (int64_t)t * c.N + n, s);
+}
+
+// ... K-major: expand[a][j][n]
+__global__ __launch_bounds__(256) void moe_lora_finish_kmajor_kernel(LoraCall c, const float* partial, int parts,
+                                                                     const float* sv) {
   const int t = blockIdx.y;
   const int n = blockIdx.x * 256 + threadIdx.x;
   if (n >= c.N) return;
@@ -168,30 +225,13 @@ __global__ __launch_bounds__(256) void moe_lora_finish_kernel(LoraCall c, const 
   for (int q = 0; q < parts; ++q) s += partial[((int64_t)q * c.T + t) * c.N + n];
   if (l >= 0) {
     const float* v = sv + (int64_t)t * c.r;  // uniform: scalar loads
+    const bf16_t* m = c.expand + (int64_t)l * c.r * c.N + n;
     float e = 0.f;
-    if constexpr (KMAJ) {
-      const bf16_t* m = c.expand + (int64_t)l * c.r * c.N + n;
 #pragma unroll 8
-      for (int j = 0; j < c.r; ++j) e = fmaf(v[j], bf16_to_f32(m[(int64_t)j * c.N]), e);
-    } else {
-      const u32x4* m = reinterpret_cast<const u32x4*>(c.expand + ((int64_t)l * c.N + n) * c.r);
-#pragma unroll 8
-      for (int j = 0; j < c.r / 8; ++j) {
-        const u32x4 b = m[j];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          e = fmaf(v[8 * j + 2 * h], __builtin_bit_cast(float, b[h] << 16), e);
-          e = fmaf(v[8 * j + 2 * h + 1], __builtin_bit_cast(float, b[h] & 0xFFFF0000u), e);
-        }
-      }
-    }
+    for (int j = 0; j < c.r; ++j) e = fmaf(v[j], bf16_to_f32(m[(int64_t)j * c.N]), e);
     s += e;
   }
-  const int64_t at = (int64_t)t * c.N + n;
-  if (c.out16)
-    static_cast<bf16_t*>(c.out)[at] = f32_to_bf16(s);
-  else
-    static_cast<float*>(c.out)[at] = s;
+  store_out(c, (int64_t)t * c.N + n, s);
 }
 
 template <int MT, bool KMAJ>
@@ -220,9 +260,17 @@ hipError_t launch_lora_decode(const LoraCall& c, bool kmajor, const ShrinkOut& o
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((c.N + 255) / 256), (unsigned)c.T);
   if (kmajor)
-    hipLaunchKernelGGL(moe_lora_finish_kernel<true>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
+    hipLaunchKernelGGL(moe_lora_finish_kmajor_kernel, grid, dim3(256), 0, s, c, partial, parts, o.sv);
+  else if (c.r <= 8)
+    hipLaunchKernelGGL(moe_lora_finish_kernel<1>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
+  else if (c.r <= 16)
+    hipLaunchKernelGGL(moe_lora_finish_kernel<2>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
+  else if (c.r <= 32)
+    hipLaunchKernelGGL(moe_lora_finish_kernel<4>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
+  else if (c.r <= 64)
+    hipLaunchKernelGGL(moe_lora_finish_kernel<8>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
   else
-    hipLaunchKernelGGL(moe_lora_finish_kernel<false>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
+    hipLaunchKernelGGL(moe_lora_finish_kernel<16>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
   return hipGetLastError();
 }
 

@@ -147,33 +147,47 @@ __device__ __forceinline__ void lora_expand(const LoraGemm& p, char* lds, int64_
   }
 }
 
-template <bool KT>
-__global__ __launch_bounds__(256) void moe_lora_prefill_kernel(LoraGemm p) {
+// The output type fixed at compile time (with both epilogues the kernels spilled).
+template <bool OUT16>
+struct TypedLora : LoraGemm {
+  static constexpr int out16 = OUT16;
+};
+
+template <bool KT, bool OUT16>
+__global__ __launch_bounds__(256) void moe_lora_prefill_kernel(TypedLora<OUT16> p) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   prefill_tile<false, false, false, KT>(p, lds);
 }
 
-__global__ __launch_bounds__(256) void moe_lora_kmajor_prefill_kernel(LoraGemm p) {
+template <bool OUT16>
+__global__ __launch_bounds__(256) void moe_lora_kmajor_prefill_kernel(TypedLora<OUT16> p) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   prefill_tile<false, false, true>(p, lds);
 }
 
 __global__ __launch_bounds__(256) void moe_lora_fixup_kernel(LoraGemm p) { fixup_tiles<false, false>(p); }
 
-template <class Kernel>
-hipError_t launch_tiles(Kernel kernel, const LoraGemm& p, int64_t blocks, std::atomic<uint64_t>& done,
-                        hipStream_t s) {
+template <bool OUT16>
+hipError_t launch_tiles(void (*kernel)(TypedLora<OUT16>), const LoraGemm& g, int64_t blocks,
+                        std::atomic<uint64_t>& done, hipStream_t s) {
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), kLdsBytes, done);
   if (e != hipSuccess) return e;
+  TypedLora<OUT16> p;
+  static_cast<LoraGemm&>(p) = g;
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), kLdsBytes, s, p);
   return hipGetLastError();
+}
+
+hipError_t launch_typed(void (*k32)(TypedLora<false>), void (*k16)(TypedLora<true>), const LoraGemm& p, int64_t blocks,
+                        std::atomic<uint64_t>& done32, std::atomic<uint64_t>& done16, hipStream_t s) {
+  return p.out16 ? launch_tiles<true>(k16, p, blocks, done16, s) : launch_tiles<false>(k32, p, blocks, done32, s);
 }
 
 }  // namespace
 
 hipError_t launch_lora_prefill(const LoraCall& c, bool kmajor, const uint16_t* parts, float* partial,
                                hipStream_t s) {
-  static std::atomic<uint64_t> done[3];
+  static std::atomic<uint64_t> done[6];
   LoraGemm p{};
   p.A = c.in;
   p.lda = c.K;
@@ -189,16 +203,22 @@ hipError_t launch_lora_prefill(const LoraCall& c, bool kmajor, const uint16_t* p
   p.partial = partial;
   hipError_t e = partial ? split_ctas(&p.ctas) : hipSuccess;
   if (e != hipSuccess) return e;
+  // the rows are known here, and with them which tiles are cut (as on the device)
   const int64_t mtiles = (c.T + BM - 1) / BM;
-  const int64_t blocks = (mtiles * p.n_tiles_n + 7) / 8 * 8 + p.ctas;
+  const Split sp = split_of(p, mtiles);
+  if (sp.R == 0) p.ctas = 0;
+  const int64_t blocks = (sp.n_dp + 7) / 8 * 8 + sp.R * sp.S;
   if (kmajor)
-    e = launch_tiles(moe_lora_kmajor_prefill_kernel, p, blocks, done[0], s);
+    e = launch_typed(moe_lora_kmajor_prefill_kernel<false>, moe_lora_kmajor_prefill_kernel<true>, p, blocks, done[0],
+                     done[3], s);
   else if (c.K % BK)
-    e = launch_tiles(moe_lora_prefill_kernel<true>, p, blocks, done[1], s);
+    e = launch_typed(moe_lora_prefill_kernel<true, false>, moe_lora_prefill_kernel<true, true>, p, blocks, done[1],
+                     done[4], s);
   else
-    e = launch_tiles(moe_lora_prefill_kernel<false>, p, blocks, done[2], s);
-  if (e != hipSuccess || p.ctas <= 0) return e;
-  hipLaunchKernelGGL(moe_lora_fixup_kernel, dim3((unsigned)p.ctas * kFixBlocksPerTile), dim3(256), 0, s, p);
+    e = launch_typed(moe_lora_prefill_kernel<false, false>, moe_lora_prefill_kernel<false, true>, p, blocks, done[2],
+                     done[5], s);
+  if (e != hipSuccess || sp.R == 0) return e;
+  hipLaunchKernelGGL(moe_lora_fixup_kernel, dim3((unsigned)(sp.R * kFixBlocksPerTile)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

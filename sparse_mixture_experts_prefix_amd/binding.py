@@ -158,6 +158,9 @@ def _ptr(t):
 
 
 def _dev(t, name, dtype, shape=None):
+    if t is not None and t.is_cuda and t.dtype is dtype and t.is_contiguous() and (
+            shape is None or t.shape == shape):
+        return t
     if t is None:
         raise ValueError("%s is required" % name)
     if not t.is_cuda:
@@ -554,8 +557,9 @@ def _dtype_code(dtype, name):
 
 
 def _same_device(first, *rest):
+    index = first.get_device()
     for t in rest:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError("all tensors must be on one device")
 
 
@@ -574,8 +578,11 @@ def _workspace(workspace, device, fn, *args):
 
 def _run(device, fn, *args):
     """Calls the library with `device` current, on its current stream."""
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, torch._C._cuda_getCurrentRawStream(device.index)))
+    index = device.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        if rc < 0:
+            _check(rc)
         return
     with torch.cuda.device(device):
         _check(fn(*args, _stream(device)))

@@ -19,7 +19,7 @@ __global__ __launch_bounds__(256) void moe_lora_shrink_kernel(LoraCall c, Shrink
   if ((int)blockIdx.x < lists)
     lora_list(c, rows, blockIdx.x, reinterpret_cast<int*>(lds));
   else
-    lora_shrink_tile<RB, KMAJ>(c, o, blockIdx.x - lists, 0, 0, 1, lds);
+    lora_shrink_tile<RB, KMAJ, false>(c, o, blockIdx.x - lists, 0, 0, 1, 0, (c.K + 63) / 64, lds);
 }
 
 template <int RB, bool KMAJ>
@@ -54,10 +54,10 @@ hipError_t launch_lora_forward(const moe_lora_shape& s, const LoraPlan& p, const
                    static_cast<const bf16_t*>(t.lora_a), static_cast<const bf16_t*>(t.lora_b), t.adapter,
                    t.scale, s.T, s.D, s.N, s.L, s.r, y, s.out_dtype == MOE_DTYPE_BF16};
   if (p.parts)
-    return launch_lora_decode(c, false, ShrinkOut{xa, at<float>(ws, p.off_sv), nullptr, nullptr, nullptr},
-                              LoraLists{}, at<float>(ws, p.off_partial), p.parts, st);
+    return launch_lora_decode(c, false, ShrinkOut{xa, nullptr, nullptr, nullptr}, LoraLists{},
+                              at<float>(ws, p.off_v), p.v_parts, at<float>(ws, p.off_partial), p.parts, st);
   uint16_t* parts = at<uint16_t>(ws, p.off_v16);
-  const hipError_t e = launch_shrink_rank<false>(c, ShrinkOut{xa, nullptr, parts, nullptr, nullptr}, LoraLists{}, st);
+  const hipError_t e = launch_shrink_rank<false>(c, ShrinkOut{xa, parts, nullptr, nullptr}, LoraLists{}, st);
   if (e != hipSuccess) return e;
   return launch_lora_prefill(c, false, parts, p.split ? at<float>(ws, p.off_partial) : nullptr, st);
 }
@@ -76,10 +76,10 @@ hipError_t launch_lora_backward(const moe_lora_shape& s, const LoraBwdPlan& p,
   float* partial = at<float>(ws, p.off_partial);
   hipError_t e;
   if (p.parts) {
-    e = launch_lora_decode(c, true, ShrinkOut{nullptr, at<float>(ws, p.off_su), u16, xa, xa16}, rows, partial,
-                           p.parts, st);
+    e = launch_lora_decode(c, true, ShrinkOut{nullptr, u16, xa, xa16}, rows, at<float>(ws, p.off_v), p.v_parts,
+                           partial, p.parts, st);
   } else {
-    e = launch_shrink_rank<true>(c, ShrinkOut{nullptr, nullptr, u16, xa, xa16}, rows, st);
+    e = launch_shrink_rank<true>(c, ShrinkOut{nullptr, u16, xa, xa16}, rows, st);
     if (e == hipSuccess) e = launch_lora_prefill(c, true, u16, p.split ? partial : nullptr, st);
   }
   if (e != hipSuccess) return e;

@@ -27,7 +27,6 @@ struct LoraLists {
 // Outputs of the first product; each but one may be NULL.
 struct ShrinkOut {
   float* v;           // fp32 [T][r], unscaled (zero rows without an adapter)
-  float* sv;          // fp32 [T][r], scaled
   uint16_t* parts;    // bf16 [T][2 r]: scaled, upper parts then lower parts
   const float* xa;    // fp32 [T][r] in ...
   uint16_t* xa_parts; // ... and its parts (all rows), written on the way

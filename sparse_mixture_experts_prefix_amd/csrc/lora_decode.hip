@@ -132,18 +132,26 @@ __device__ __forceinline__ void project_tile(const LoraCall& c, int n0, int q0, 
 struct FewRows {
   int shrink, lists;  // workgroups of the first product, and of the rows' lists
   int tiles, parts;   // column tiles, parts of K
+  int v_parts;        // parts of K of the first product
+  float* v;           // [v_parts][T][r]
   float* partial;     // [parts][T][N]
 };
 
-// Workgroups: the first product, one per block of 16 ranks, tile of 16 rows and slot
-// of 16 (the tile's distinct adapters); the rows' lists; the projection.
+// Workgroups: the first product, one per block of 16 ranks, tile of 16 rows, part of K
+// and slot of 16 (the tile's distinct adapters); the rows' lists; the projection.  The
+// first product's parts are short, so that all of a wave's loads are in flight from the
+// start: beside the weights' stream each wait takes several microseconds (whole rows
+// of 4096 k took 11.3 us with the projection, which alone takes 8.2).
 template <int MT, bool KMAJ>
 __global__ __launch_bounds__(256) void moe_lora_decode_kernel(LoraCall c, ShrinkOut o, LoraLists rows, FewRows f) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   int b = blockIdx.x;
   if (b < f.shrink) {
-    const int tiles = (c.T + 15) / 16, u = b / 16;
-    lora_shrink_tile<1, KMAJ>(c, o, u % tiles, u / tiles, b % 16, 16, lds);
+    const int tiles = (c.T + 15) / 16, u = b / 16, q = u / tiles, part = q % f.v_parts, nq = (c.K + 63) / 64;
+    ShrinkOut op = o;
+    op.v = f.v + (int64_t)part * c.T * c.r;
+    lora_shrink_tile<1, KMAJ, true>(c, op, u % tiles, q / f.v_parts, b % 16, 16, (int)((int64_t)part * nq / f.v_parts),
+                                    (int)((int64_t)(part + 1) * nq / f.v_parts), lds);
     return;
   }
   b -= f.shrink;
@@ -165,29 +173,59 @@ __device__ __forceinline__ void store_out(const LoraCall& c, int64_t at, float v
     static_cast<float*>(c.out)[at] = v;
 }
 
+// The row's first product at rank j: its parts added in order.
+__device__ __forceinline__ float sum_v(const LoraCall& c, const FewRows& f, int t, int j) {
+  float v = f.v[(int64_t)t * c.r + j];
+  for (int q = 1; q < f.v_parts; ++q) v += f.v[((int64_t)q * c.T + t) * c.r + j];
+  return v;
+}
+// ... kept where asked for, by the row's first workgroup.
+__device__ __forceinline__ void keep_v(const LoraCall& c, const ShrinkOut& o, const FewRows& f, int t, int l) {
+  const int j = threadIdx.x;
+  if (blockIdx.x != 0 || j >= c.r) return;
+  const float v = l >= 0 ? sum_v(c, f, t, j) : 0.f;
+  if (o.v) o.v[(int64_t)t * c.r + j] = v;
+  if (o.parts) {
+    const float s = l >= 0 ? v * lora_scale(c, l) : 0.f;
+    split_bf16(s, o.parts[(int64_t)t * 2 * c.r + j], o.parts[(int64_t)t * 2 * c.r + c.r + j]);
+  }
+}
+
+__device__ __forceinline__ float sum_parts(const LoraCall& c, const FewRows& f, int t, int n) {
+  float s = 0.f;
+#pragma unroll 4
+  for (int q = 0; q < f.parts; ++q) s += f.partial[((int64_t)q * c.T + t) * c.N + n];
+  return s;
+}
+
 // out[t][n] = sum of the parts (in part order) + sum_j sv[t][j] expand[a][n][j], one
 // row and 256 columns per workgroup.  G lanes share a row of expand (16 bytes each, 8 G >=
 // r), so a wave's loads are one contiguous piece (a row per lane read 16 bytes of 64
-// different lines per load: 11 us against 8 us at 64 rows x 5760 columns, rank 64); the
+// different lines per load: 11 us against 10 us at 64 rows x 5760 columns, rank 64); the
 // lanes' sums are added in a fixed tree.
-template <int G>
-__global__ __launch_bounds__(256) void moe_lora_finish_kernel(LoraCall c, const float* partial, int parts,
-                                                              const float* sv) {
+template <int G, int VP>
+__global__ __launch_bounds__(256) void moe_lora_finish_kernel(LoraCall c, ShrinkOut o, FewRows f) {
   __shared__ float es[256];
   const int t = blockIdx.y, lane = threadIdx.x & 63, w0 = threadIdx.x & ~63;
   const int n0 = blockIdx.x * 256 + w0;  // first column of this wave
   const int l = lora_id(c, t);
-  const int n = n0 + lane;
-  float s = 0.f;
-  if (n < c.N) {
-#pragma unroll 4
-    for (int q = 0; q < parts; ++q) s += partial[((int64_t)q * c.T + t) * c.N + n];
-  }
+  const int n = n0 + lane, g = lane % G, row = lane / G;
+  float s = n < c.N ? sum_parts(c, f, t, n) : 0.f;
   if (l >= 0) {  // uniform
-    const int g = lane % G, row = lane / G;
+    const float sc = lora_scale(c, l);
     float v[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = 8 * g < c.r ? sv[(int64_t)t * c.r + 8 * g + u] : 0.f;
+    for (int u = 0; u < 8; ++u) v[u] = 0.f;
+    if (8 * g < c.r) {
+#pragma unroll
+      for (int q = 0; q < VP; ++q) {
+        const float4* src = reinterpret_cast<const float4*>(f.v + ((int64_t)q * c.T + t) * c.r + 8 * g);
+        const float4 x = src[0], y = src[1];
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] *= sc;
     u32x4 b[G];
 #pragma unroll
     for (int i = 0; i < G; ++i) {
@@ -211,24 +249,23 @@ __global__ __launch_bounds__(256) void moe_lora_finish_kernel(LoraCall c, const 
     s += es[threadIdx.x];
   }
   if (n < c.N) store_out(c, (int64_t)t * c.N + n, s);
+  if (o.v || o.parts) keep_v(c, o, f, t, l);
 }
 
-// ... K-major: expand[a][j][n]
-__global__ __launch_bounds__(256) void moe_lora_finish_kmajor_kernel(LoraCall c, const float* partial, int parts,
-                                                                     const float* sv) {
+// ... K-major: expand[a][j][n] (the row's v is the same for all: scalar loads)
+__global__ __launch_bounds__(256) void moe_lora_finish_kmajor_kernel(LoraCall c, ShrinkOut o, FewRows f) {
   const int t = blockIdx.y;
   const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= c.N) return;
   const int l = lora_id(c, t);
-  float s = 0.f;
-#pragma unroll 4
-  for (int q = 0; q < parts; ++q) s += partial[((int64_t)q * c.T + t) * c.N + n];
+  keep_v(c, o, f, t, l);
+  if (n >= c.N) return;
+  float s = sum_parts(c, f, t, n);
   if (l >= 0) {
-    const float* v = sv + (int64_t)t * c.r;  // uniform: scalar loads
     const bf16_t* m = c.expand + (int64_t)l * c.r * c.N + n;
+    const float sc = lora_scale(c, l);
     float e = 0.f;
 #pragma unroll 8
-    for (int j = 0; j < c.r; ++j) e = fmaf(v[j], bf16_to_f32(m[(int64_t)j * c.N]), e);
+    for (int j = 0; j < c.r; ++j) e = fmaf(sum_v(c, f, t, j) * sc, bf16_to_f32(m[(int64_t)j * c.N]), e);
     s += e;
   }
   store_out(c, (int64_t)t * c.N + n, s);
@@ -245,11 +282,21 @@ hipError_t launch(const LoraCall& c, const ShrinkOut& o, const LoraLists& rows, 
   return hipGetLastError();
 }
 
+template <int G>
+hipError_t launch_finish(const LoraCall& c, const ShrinkOut& o, const FewRows& f, dim3 grid, hipStream_t s) {
+  if (f.v_parts == 2)
+    hipLaunchKernelGGL((moe_lora_finish_kernel<G, 2>), grid, dim3(256), 0, s, c, o, f);
+  else
+    hipLaunchKernelGGL((moe_lora_finish_kernel<G, 1>), grid, dim3(256), 0, s, c, o, f);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_lora_decode(const LoraCall& c, bool kmajor, const ShrinkOut& o, const LoraLists& rows,
-                              float* partial, int parts, hipStream_t s) {
-  const FewRows f{(c.T + 15) / 16 * ((c.r + 15) / 16) * 16, rows.counts ? c.L : 0, (c.N + 63) / 64, parts, partial};
+                              float* v, int v_parts, float* partial, int parts, hipStream_t s) {
+  const FewRows f{(c.T + 15) / 16 * ((c.r + 15) / 16) * v_parts * 16, rows.counts ? c.L : 0, (c.N + 63) / 64,
+                  parts, v_parts, v, partial};
   hipError_t e;
   if (c.T <= 16)
     e = kmajor ? launch<1, true>(c, o, rows, f, s) : launch<1, false>(c, o, rows, f, s);
@@ -259,19 +306,15 @@ hipError_t launch_lora_decode(const LoraCall& c, bool kmajor, const ShrinkOut& o
     e = kmajor ? launch<4, true>(c, o, rows, f, s) : launch<4, false>(c, o, rows, f, s);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((c.N + 255) / 256), (unsigned)c.T);
-  if (kmajor)
-    hipLaunchKernelGGL(moe_lora_finish_kmajor_kernel, grid, dim3(256), 0, s, c, partial, parts, o.sv);
-  else if (c.r <= 8)
-    hipLaunchKernelGGL(moe_lora_finish_kernel<1>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
-  else if (c.r <= 16)
-    hipLaunchKernelGGL(moe_lora_finish_kernel<2>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
-  else if (c.r <= 32)
-    hipLaunchKernelGGL(moe_lora_finish_kernel<4>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
-  else if (c.r <= 64)
-    hipLaunchKernelGGL(moe_lora_finish_kernel<8>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
-  else
-    hipLaunchKernelGGL(moe_lora_finish_kernel<16>, grid, dim3(256), 0, s, c, partial, parts, o.sv);
-  return hipGetLastError();
+  if (kmajor) {
+    hipLaunchKernelGGL(moe_lora_finish_kmajor_kernel, grid, dim3(256), 0, s, c, o, f);
+    return hipGetLastError();
+  }
+  if (c.r <= 8) return launch_finish<1>(c, o, f, grid, s);
+  if (c.r <= 16) return launch_finish<2>(c, o, f, grid, s);
+  if (c.r <= 32) return launch_finish<4>(c, o, f, grid, s);
+  if (c.r <= 64) return launch_finish<8>(c, o, f, grid, s);
+  return launch_finish<16>(c, o, f, grid, s);
 }
 
 }  // namespace moe

@@ -40,9 +40,11 @@ __device__ __forceinline__ void shrink_wait() {
 
 // Ranks 16 rb .. 16 (rb + RB) - 1 (those below r).  slot, slots: this workgroup
 // takes the tile's distinct adapters slot, slot + slots, ... (in order of first row).
-template <int RB, bool KMAJ>
+// Chunks q0 .. q1 - 1 of K; PART: their sums go to o.v as they are (rows without an
+// adapter are left out), to be added up by the caller's next kernel.
+template <int RB, bool KMAJ, bool PART>
 __device__ __forceinline__ void lora_shrink_tile(const LoraCall& c, const ShrinkOut& o, int tile, int rb,
-                                                 int slot, int slots, char* lds) {
+                                                 int slot, int slots, int q0, int q1, char* lds) {
   constexpr int S = shrink_stages<RB>(), SB = shrink_stage_bytes<RB>(), V = 2 + 2 * RB;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -50,11 +52,11 @@ __device__ __forceinline__ void lora_shrink_tile(const LoraCall& c, const Shrink
   const int64_t t0 = (int64_t)tile * 16;
   const int rows = (int)min((int64_t)16, c.T - t0);
   const int my = col < rows ? lora_id(c, t0 + col) : -1;  // adapter of row `col`, in every lane group
-  if (slot == 0 && rb == 0 && o.v) {  // rows without an adapter
+  if (!PART && slot == 0 && rb == 0 && o.v) {  // rows without an adapter
     for (int e = threadIdx.x; e < rows * c.r; e += blockDim.x)
       if (lora_id(c, t0 + e / c.r) < 0) o.v[t0 * c.r + e] = 0.f;
   }
-  if (slot == 0 && rb == 0 && o.xa) {
+  if (slot == 0 && rb == 0 && q0 == 0 && o.xa) {
     for (int e = threadIdx.x; e < rows * c.r; e += blockDim.x) {
       const int64_t t = t0 + e / c.r;
       const int j = e % c.r;
@@ -65,7 +67,7 @@ __device__ __forceinline__ void lora_shrink_tile(const LoraCall& c, const Shrink
   uint32_t left = (uint32_t)__ballot(lane < 16 && my >= 0);
   const __amdgpu_buffer_rsrc_t rsX = lora_rsrc(c.in + t0 * c.K, (uint32_t)(rows * c.K * 2));
   char* ring = lds + wave * (S * SB);
-  const int nq = (c.K + 63) / 64;
+  const int nq = q1 - q0;
   const int nm = wave < nq ? (nq - 1 - wave) / kShrinkWaves + 1 : 0;  // this wave's chunks
   for (int n = 0; left; ++n) {
     const int l = __builtin_amdgcn_readlane(my, __builtin_ctz(left));
@@ -79,7 +81,7 @@ __device__ __forceinline__ void lora_shrink_tile(const LoraCall& c, const Shrink
         lora_rsrc(c.shrink + (int64_t)l * c.r * c.K, (uint32_t)(c.r * c.K * 2));
     // chunk m of this wave into ring slot s; loads past K or the ranks bring zeros
     auto issue = [&](int m, int s) {
-      const int k0 = (wave + kShrinkWaves * m) * 64;
+      const int k0 = (q0 + wave + kShrinkWaves * m) * 64;
       char* st = ring + __builtin_amdgcn_readfirstlane(s * SB);
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
@@ -164,9 +166,9 @@ __device__ __forceinline__ void lora_shrink_tile(const LoraCall& c, const Shrink
           const int row = 4 * gq + i;
           if (!((same >> row) & 1)) continue;
           const int64_t t = t0 + row;
-          if (o.v) o.v[t * c.r + j] = acc[b][i];
+          if (PART || o.v) o.v[t * c.r + j] = acc[b][i];
+          if constexpr (PART) continue;
           const float v = acc[b][i] * sc;
-          if (o.sv) o.sv[t * c.r + j] = v;
           if (o.parts) {
             bf16_t hi, lo;
             split_bf16(v, hi, lo);

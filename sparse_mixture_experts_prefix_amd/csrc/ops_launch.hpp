@@ -27,10 +27,10 @@ hipError_t launch_lora_backward(const moe_lora_shape& s, const LoraBwdPlan& p,
 // bf16 parts; partial (or NULL: no cut along K) room for partial tiles.
 hipError_t launch_lora_prefill(const LoraCall& c, bool kmajor, const uint16_t* parts16, float* partial,
                                hipStream_t s);
-// At most 64 rows, both products (o.sv is needed); rows.counts set: the rows' lists
-// too.  partial: fp32 [parts][T][N].
+// At most 64 rows, both products; rows.counts set: the rows' lists too.  Workspace:
+// v fp32 [v_parts][T][r], partial fp32 [parts][T][N].
 hipError_t launch_lora_decode(const LoraCall& c, bool kmajor, const ShrinkOut& o, const LoraLists& rows,
-                              float* partial, int parts, hipStream_t s);
+                              float* v, int v_parts, float* partial, int parts, hipStream_t s);
 hipError_t launch_lora_wgrad(const LoraLists& rows, const void* x, const void* dy, const uint16_t* u,
                              const uint16_t* xa, const float* scale, int T, int D, int N, int L, int r,
                              float* da, float* db, hipStream_t s);

@@ -32,10 +32,10 @@ int main() {
             moe::LoraBwdPlan b;
             if (moe::make_lora_plan(&s, &p) == 0) {
               ++accepted;
-              if (!ordered({p.off_sv, p.off_v16, p.off_partial}, p.total)) return 3;
+              if (!ordered({p.off_v, p.off_v16, p.off_partial}, p.total)) return 3;
             }
             if (moe::make_lora_backward_plan(&s, &b) == 0 &&
-                !ordered({b.off_su, b.off_u16, b.off_xa16, b.off_rows, b.off_partial}, b.total))
+                !ordered({b.off_v, b.off_u16, b.off_xa16, b.off_rows, b.off_partial}, b.total))
               return 4;
           }
           moe::OrthPlan o;

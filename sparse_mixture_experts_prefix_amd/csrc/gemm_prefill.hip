@@ -133,7 +133,7 @@ hipError_t launch(bool gate_up, const GroupedGemm& g, hipStream_t s) {
 // ------------------------------------------------------------ weight gradients
 __global__ __launch_bounds__(256) void moe_gemm_wgrad_kernel(WgradGemm p) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  wgrad_whole_tile(p, blockIdx.x, lds);
+  wgrad_whole_tile<false>(p, blockIdx.x, lds);
 }
 
 // The same products when every group has at most 64 rows (a token picks an
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(256) void moe_gemm_wgrad_one_stage_kernel(WgradGemm
         wgrad_issue(p, wn_, lds, true, 0, buf ^ 1, 0, 8, wave, lane);
       }
     }
-    if (w.valid) wgrad_store(w, wm, wn, lane, acc);
+    if (w.valid) wgrad_store<false>(w, wm, wn, lane, acc);
     buf ^= 1;
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);  // no load may still be writing LDS at exit

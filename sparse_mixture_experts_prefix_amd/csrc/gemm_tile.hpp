@@ -982,7 +982,7 @@ __device__ __forceinline__ void prefill_tile(const P& p, char* lds) {
         const int n = n0 + wn * 128 + j * 32 + lr;
         voff[j] = n < N ? (uint32_t)((4 * kh * p.ldc + n) * 4) : kOob;
       }
-      auto store_rows = [&](const bool check) {
+      auto store_rows = [&](const bool check, auto policy) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (i >= act) continue;
@@ -995,15 +995,30 @@ __device__ __forceinline__ void prefill_tile(const P& p, char* lds) {
             for (int j = 0; j < 4; ++j) {
               const float v = acc[i][j][r];  // a scalar first (see the pieces' stores)
               __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rsY,
-                                                    ok ? voff[j] : kOob, soff, 0);
+                                                    ok ? voff[j] : kOob, soff,
+                                                    decltype(policy)::value);
             }
           }
         }
       };
-      if (valid_rows >= BM)
-        store_rows(false);
-      else
-        store_rows(true);
+      using Plain = std::integral_constant<int, 0>;
+      using Stream = std::integral_constant<int, 2>;  // non-temporal
+      if constexpr (P::kRagged) {
+        if (p.stream_out) {
+          if (valid_rows >= BM)
+            store_rows(false, Stream{});
+          else
+            store_rows(true, Stream{});
+        } else if (valid_rows >= BM) {
+          store_rows(false, Plain{});
+        } else {
+          store_rows(true, Plain{});
+        }
+      } else if (valid_rows >= BM) {
+        store_rows(false, Plain{});
+      } else {
+        store_rows(true, Plain{});
+      }
       if constexpr (XRT) {  // folded rows: column blocks 2 wm, 2 wm + 1 of this wave's half
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -1208,6 +1223,8 @@ __device__ __forceinline__ void wgrad_issue(const P& p, const WgradTile& w, char
 // the wave-uniform row offset in the scalar offset, the lane's column (and
 // 4-row half) in the vector offset, and rows past the matrix dropped through
 // an out-of-range vector offset (the scalar offset is not range-checked).
+// NT: non-temporal stores.
+template <bool NT>
 __device__ __forceinline__ void wgrad_store(const WgradTile& w, int wm, int wn, int lane,
                                             const f32x16 (&acc)[4][4]) {
   const int lr = lane & 31, kh = lane >> 5;
@@ -1232,7 +1249,7 @@ __device__ __forceinline__ void wgrad_store(const WgradTile& w, int wm, int wn, 
         for (int j = 0; j < 4; ++j) {
           const float v = acc[i][j][r];  // a scalar first (see the pieces' stores)
           __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rs,
-                                                ok ? voff[j] : kOob, soff, 0);
+                                                ok ? voff[j] : kOob, soff, NT ? 2 : 0);
         }
       }
   };
@@ -1259,7 +1276,7 @@ __device__ __forceinline__ void zero_acc(f32x16 (&acc)[4][4]) {
 // K-major (the rows are the reduction): both operands through the
 // transposing LDS reads, the loads written out (see lds_dma16).  A group with
 // no rows stores zeros.
-template <class P>
+template <bool NT, class P>
 __device__ __forceinline__ void wgrad_whole_tile(const P& p, int64_t t, char* lds) {
   const WgradTile w = wgrad_tile(p, t);
   if (!w.valid) return;
@@ -1298,7 +1315,7 @@ __device__ __forceinline__ void wgrad_whole_tile(const P& p, int64_t t, char* ld
     k_loop<false, 4, false, decltype(issue_a), decltype(issue_b), true, true>(
         lds, 0, (w.K + BK - 1) / BK, wm, wn, false, lane, issue_a, issue_b, acc);
   }
-  wgrad_store(w, wm, wn, lane, acc);
+  wgrad_store<NT>(w, wm, wn, lane, acc);
 }
 
 }  // namespace

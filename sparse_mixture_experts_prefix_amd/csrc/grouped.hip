@@ -133,6 +133,9 @@ hipError_t launch_grouped_gemm(const moe_gemm_shape& s, const GemmPlan& plan, co
   p.C = y;
   p.ldc = s.N;
   p.out16 = s.out_dtype == MOE_DTYPE_BF16;
+  // a y beyond the 256 MB Infinity Cache would only push the weights out of it (10007 x
+  // 7168, 64 groups of width 2048: 478 -> 453 us); a smaller one may stay for its reader
+  p.stream_out = (int64_t)s.R * s.N * 4 > (int64_t(256) << 20);
   // m-tiles that can hold rows: full ones and one ragged end per group
   int64_t mtiles = s.R / plan.BM + s.G;
   if (mtiles > s.R) mtiles = s.R;

@@ -18,7 +18,7 @@ struct LoraGemm {
   static constexpr uint16_t* gu_out = nullptr;
   static constexpr const void* B_shared = nullptr;
   static constexpr const float *S_shared = nullptr, *S_routed = nullptr;
-  static constexpr int N_shared = 0, K_shared = 0, BM = 256, E = 1;
+  static constexpr int N_shared = 0, K_shared = 0, BM = 256, E = 1, stream_out = 0;
   const uint16_t* A;
   int64_t lda;
   const void* B_routed;

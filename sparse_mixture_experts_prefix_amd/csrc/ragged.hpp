@@ -37,7 +37,8 @@ struct RaggedGemm {
   int R;
   void* C;
   int64_t ldc;
-  int out16;  // C is bf16 (else fp32)
+  int out16;       // C is bf16 (else fp32)
+  int stream_out;  // fp32 C is stored non-temporal
   int64_t n_tiles_n;
   int ctas;
   float* partial;

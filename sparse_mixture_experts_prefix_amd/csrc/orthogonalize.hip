@@ -168,96 +168,121 @@ __device__ __forceinline__ bool orth_tile(const OrthProduct& p, int64_t b, OrthT
   return true;
 }
 
-// The addends of eight results (c0 and c1 at element i), and the results: all
-// reads and writes are 16 bytes wide.
+// The addends of eight results (c0, and c1 where SYM is false, at element i), and the
+// results: all reads and writes are 16 bytes wide.
+template <bool SYM>
 struct Addend {
   f16x8 h, l;
 };
-__device__ __forceinline__ Addend load_addend(const OrthProduct& p, int64_t i, bool in) {
-  Addend a;
+template <>
+struct Addend<true> {
+  f16x8 h;
+};
+template <bool SYM>
+__device__ __forceinline__ Addend<SYM> load_addend(const OrthProduct& p, int64_t i, bool in) {
+  Addend<SYM> a;
 #pragma unroll
-  for (int u = 0; u < 8; ++u) a.h[u] = a.l[u] = (f16)0.f;
-  if (in && p.c0) a.h = *reinterpret_cast<const f16x8*>(p.c0 + i);
-  if (in && p.c1) a.l = *reinterpret_cast<const f16x8*>(p.c1 + i);
+  for (int u = 0; u < 8; ++u) a.h[u] = (f16)0.f;
+  if constexpr (SYM) {
+    if (in && p.c0) a.h = *reinterpret_cast<const f16x8*>(p.c0 + i);
+  } else {
+    a.l = a.h;
+    if (in) {
+      a.h = *reinterpret_cast<const f16x8*>(p.c0 + i);
+      a.l = *reinterpret_cast<const f16x8*>(p.c1 + i);
+    }
+  }
   return a;
 }
-__device__ __forceinline__ void emit8(const OrthProduct& p, int64_t i, const Addend& a, float (&v)[8]) {
-#pragma unroll
-  for (int u = 0; u < 8; ++u) v[u] = fmaf(p.beta, (float)a.h[u] + (float)a.l[u], v[u] * p.alpha);
-  if (p.out) {
-    u32x4 w;
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      w[u] = (uint32_t)f32_to_bf16(v[2 * u] * p.gamma) | ((uint32_t)f32_to_bf16(v[2 * u + 1] * p.gamma) << 16);
-    st16(p.out + i, w);
-    return;
-  }
-  f16x8 h, l;
+// v becomes the result
+template <bool SYM>
+__device__ __forceinline__ void emit8(const OrthProduct& p, int64_t i, const Addend<SYM>& a, float (&v)[8]) {
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    h[u] = (f16)v[u];
-    l[u] = (f16)(v[u] - (float)h[u]);
+    float x = (float)a.h[u];
+    if constexpr (!SYM) x += (float)a.l[u];
+    v[u] = fmaf(p.beta, x, v[u] * p.alpha);
   }
+  if constexpr (!SYM) {
+    if (p.out) {
+      u32x4 w;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        w[u] = (uint32_t)f32_to_bf16(v[2 * u] * p.gamma) | ((uint32_t)f32_to_bf16(v[2 * u + 1] * p.gamma) << 16);
+      st16(p.out + i, w);
+      return;
+    }
+  }
+  f16x8 h;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) h[u] = (f16)v[u];
   *reinterpret_cast<f16x8*>(p.d0 + i) = h;
-  if (p.d1) *reinterpret_cast<f16x8*>(p.d1 + i) = l;
+  if constexpr (!SYM) {
+    f16x8 l;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) l[u] = (f16)(v[u] - (float)h[u]);
+    *reinterpret_cast<f16x8*>(p.d1 + i) = l;
+  }
 }
 
-// A tile of ROWS x TS results in LDS (fp32, rows of TS + 8 so that the lanes' column
-// and row accesses spread over the banks) at rows m, columns n of the result:
-// stored row by row, and (mirror) column by column as rows of the transposed place
-// (c0 is symmetric too, so the transposed place's own c0 serves there).  Four
-// pieces per thread at a time, their addends' loads together: one after the other
-// each waited out a memory latency (X step of update_square 1.93 ms, then 1.5 ms).
+// The results of ROWS x TS accumulators at rows m, columns n: fill(tile) writes them to
+// LDS (fp32, rows of TS + 8 so that row and column accesses spread over the banks),
+// from where they leave in 16-byte rows; mirror: also as rows of the transposed place.
+// A tile's end is not hidden behind another tile (the accumulators allow one
+// workgroup per CU), so its waits count: all addends of the piece are requested before
+// the accumulators go to LDS, and the transposed rows are made of finished results.
+// (Addends loaded four at a time as they were needed, and again for the transposed
+// place: a third of the X step's time and 40% of the symmetric products'.)
 template <int TS>
 constexpr int tile_pitch() { return TS + 8; }
-template <int ROWS, int TS>
-__device__ __forceinline__ void emit_tile(const OrthProduct& p, int64_t at, int m, int n, const float* tile,
-                                          bool mirror) {
+template <bool SYM, int ROWS, int TS, class Fill>
+__device__ __forceinline__ void emit_tile(const OrthProduct& p, int64_t at, int m, int n, float* tile, bool mirror,
+                                          Fill fill) {
   const int rows = min(ROWS, p.M - m), cols = min(TS, p.N - n);  // multiples of 8
-  constexpr int PIECES = ROWS * TS / 8 / 256, U = PIECES < 4 ? PIECES : 4;
-  static_assert(PIECES % U == 0, "whole batches");
-#pragma unroll 1
-  for (int q0 = 0; q0 < PIECES; q0 += U) {
-    Addend a[U];
+  constexpr int PIECES = ROWS * TS / 8 / 256;
+  Addend<SYM> a[PIECES];
+  const int64_t base = at + (int64_t)m * p.N + n;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int q = (q0 + u) * 256 + threadIdx.x, r = q / (TS / 8), c = q % (TS / 8) * 8;
-      a[u] = load_addend(p, at + (int64_t)(m + r) * p.N + n + c, r < rows && c < cols);
-    }
+  for (int u = 0; u < PIECES; ++u) {
+    const int q = u * 256 + threadIdx.x, r = q / (TS / 8), c = q % (TS / 8) * 8;
+    a[u] = load_addend<SYM>(p, base + (int64_t)r * p.N + c, r < rows && c < cols);
+  }
+  fill(tile);
+  __syncthreads();
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int q = (q0 + u) * 256 + threadIdx.x, r = q / (TS / 8), c = q % (TS / 8) * 8;
-      if (r >= rows || c >= cols) continue;
-      float v[8];
-      const float4 x = *reinterpret_cast<const float4*>(tile + r * tile_pitch<TS>() + c);
-      const float4 y = *reinterpret_cast<const float4*>(tile + r * tile_pitch<TS>() + c + 4);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-      emit8(p, at + (int64_t)(m + r) * p.N + n + c, a[u], v);
+  for (int u = 0; u < PIECES; ++u) {
+    const int q = u * 256 + threadIdx.x, r = q / (TS / 8), c = q % (TS / 8) * 8;
+    if (r >= rows || c >= cols) continue;
+    float* src = tile + r * tile_pitch<TS>() + c;
+    float v[8];
+    const float4 x = *reinterpret_cast<const float4*>(src);
+    const float4 y = *reinterpret_cast<const float4*>(src + 4);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    emit8<SYM>(p, base + (int64_t)r * p.N + c, a[u], v);
+    if constexpr (SYM) {
+      if (mirror) {
+        *reinterpret_cast<float4*>(src) = float4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<float4*>(src + 4) = float4{v[4], v[5], v[6], v[7]};
+      }
     }
   }
-  if (!mirror) return;
-#pragma unroll 1
-  for (int q0 = 0; q0 < PIECES; q0 += U) {
-    Addend a[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int q = (q0 + u) * 256 + threadIdx.x, c = q % TS, r = q / TS * 8;
-      a[u] = load_addend(p, at + (int64_t)(n + c) * p.N + m + r, r < rows && c < cols);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int q = (q0 + u) * 256 + threadIdx.x, c = q % TS, r = q / TS * 8;
+  if constexpr (SYM) {
+    if (!mirror) return;
+    __syncthreads();
+#pragma unroll 4
+    for (int u = 0; u < PIECES; ++u) {
+      const int q = u * 256 + threadIdx.x, c = q % TS, r = q / TS * 8;
       if (r >= rows || c >= cols) continue;
-      float v[8];
+      f16x8 h;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) v[w] = tile[(r + w) * tile_pitch<TS>() + c];
-      emit8(p, at + (int64_t)(n + c) * p.N + m + r, a[u], v);
+      for (int w = 0; w < 8; ++w) h[w] = (f16)tile[(r + w) * tile_pitch<TS>() + c];
+      *reinterpret_cast<f16x8*>(p.d0 + at + (int64_t)(n + c) * p.N + m + r) = h;
     }
   }
 }
 
 // 256 x 256 tiles.  KB: B is K-major, KA: A is too.
-template <bool KA, bool KB>
+template <bool KA, bool KB, bool SYM>
 __global__ __launch_bounds__(256) void moe_orth_tile256_kernel(OrthProduct p) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   OrthTile t;
@@ -361,19 +386,20 @@ __global__ __launch_bounds__(256) void moe_orth_tile256_kernel(OrthProduct p) {
   for (int half = 0; half < 2; ++half) {
     if (half * 128 >= valid) break;
     __syncthreads();  // the K loop's reads, or the first half's, are done
+    emit_tile<SYM, 128, 256>(
+        p, (int64_t)t.e * p.M * p.N, t.m0 + 128 * half, t.n0, tile, SYM && t.m0 != t.n0, [&](float* d) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = a_row_of(wm, i, il) - 128 * half;
-      if (row < 0 || row >= 128) continue;
+          for (int i = 0; i < 4; ++i) {
+            const int row = a_row_of(wm, i, il) - 128 * half;
+            if (row < 0 || row >= 128) continue;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          tile[(row + 8 * (r >> 2) + 4 * kh + (r & 3)) * tile_pitch<256>() + b_row_of<false>(wn, j) + lr] =
-              acc[i][j][r];
-    }
-    __syncthreads();
-    emit_tile<128, 256>(p, (int64_t)t.e * p.M * p.N, t.m0 + 128 * half, t.n0, tile, p.sym && t.m0 != t.n0);
+              for (int r = 0; r < 16; ++r)
+                d[(row + 8 * (r >> 2) + 4 * kh + (r & 3)) * tile_pitch<256>() + b_row_of<false>(wn, j) + lr] =
+                    acc[i][j][r];
+          }
+        });
   }
 }
 
@@ -381,7 +407,7 @@ __global__ __launch_bounds__(256) void moe_orth_tile256_kernel(OrthProduct p) {
 // in LDS, two of them in flight.  Two workgroups share a CU's registers but not its
 // LDS; taken where the 256 x 256 tiles are too few for the chip.
 constexpr int kStage128 = 2 * 128 * BK * 2;
-template <bool KA, bool KB>
+template <bool KA, bool KB, bool SYM>
 __global__ __launch_bounds__(256) void moe_orth_tile128_kernel(OrthProduct p) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   OrthTile t;
@@ -481,21 +507,21 @@ __global__ __launch_bounds__(256) void moe_orth_tile128_kernel(OrthProduct p) {
   float* tile = reinterpret_cast<float*>(lds);
   static_assert(128 * tile_pitch<128>() * 4 <= 3 * kStage128, "the results must fit");
   __syncthreads();  // the last stage's reads are done
+  emit_tile<SYM, 128, 128>(p, (int64_t)t.e * p.M * p.N, t.m0, t.n0, tile, SYM && t.m0 != t.n0, [&](float* d) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        tile[(wm * 64 + 32 * i + 8 * (r >> 2) + 4 * kh + (r & 3)) * tile_pitch<128>() + wn * 64 + 32 * j + lr] =
-            acc[i][j][r];
-  __syncthreads();
-  emit_tile<128, 128>(p, (int64_t)t.e * p.M * p.N, t.m0, t.n0, tile, p.sym && t.m0 != t.n0);
+        for (int r = 0; r < 16; ++r)
+          d[(wm * 64 + 32 * i + 8 * (r >> 2) + 4 * kh + (r & 3)) * tile_pitch<128>() + wn * 64 + 32 * j + lr] =
+              acc[i][j][r];
+  });
 }
 
 // Finishes the cut tiles, 16 rows of one per workgroup: the pieces' sums are added
 // in K order.
-template <int TS>
+template <int TS, bool SYM>
 __global__ __launch_bounds__(256) void moe_orth_fixup_kernel(OrthProduct p) {
   __shared__ float tile[16 * tile_pitch<TS>()];
   const int k = blockIdx.x / (TS / 16), r0 = blockIdx.x % (TS / 16) * 16;
@@ -505,44 +531,44 @@ __global__ __launch_bounds__(256) void moe_orth_fixup_kernel(OrthProduct p) {
   orth_coords(p, (int)(L - (int64_t)e * p.per), ti, tj);
   if (ti * TS + r0 >= p.M) return;
   const float* P = p.partial + ((int64_t)k * p.S * TS + r0) * TS;
-  for (int q = threadIdx.x; q < 16 * TS / 4; q += 256) {
-    const float4* src = reinterpret_cast<const float4*>(P) + q;
-    float4 a = src[0];
-    for (int s = 1; s < p.S; ++s) {
-      const float4 b = src[(int64_t)s * TS * TS / 4];
-      a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+  emit_tile<SYM, 16, TS>(p, (int64_t)e * p.M * p.N, ti * TS + r0, tj * TS, tile, SYM && ti != tj, [&](float* d) {
+    for (int q = threadIdx.x; q < 16 * TS / 4; q += 256) {
+      const float4* src = reinterpret_cast<const float4*>(P) + q;
+      float4 a = src[0];
+      for (int s = 1; s < p.S; ++s) {
+        const float4 b = src[(int64_t)s * TS * TS / 4];
+        a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+      }
+      *reinterpret_cast<float4*>(d + q * 4 / TS * tile_pitch<TS>() + q * 4 % TS) = a;
     }
-    *reinterpret_cast<float4*>(tile + q * 4 / TS * tile_pitch<TS>() + q * 4 % TS) = a;
-  }
-  __syncthreads();
-  emit_tile<16, TS>(p, (int64_t)e * p.M * p.N, ti * TS + r0, tj * TS, tile, p.sym && ti != tj);
+  });
 }
 
-template <int TS, bool KA, bool KB>
+template <int TS, bool KA, bool KB, bool SYM>
 hipError_t launch_tiles(const OrthProduct& p, hipStream_t s) {
   static std::atomic<uint64_t> done;
   constexpr int lds = TS == 256 ? kLdsBytes : 3 * kStage128;
   void (*kernel)(OrthProduct);
   if constexpr (TS == 256)
-    kernel = moe_orth_tile256_kernel<KA, KB>;
+    kernel = moe_orth_tile256_kernel<KA, KB, SYM>;
   else
-    kernel = moe_orth_tile128_kernel<KA, KB>;
+    kernel = moe_orth_tile128_kernel<KA, KB, SYM>;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), lds, done);
   if (e != hipSuccess) return e;
   const int64_t blocks = (p.n_dp + 7) / 8 * 8 + (int64_t)p.R * p.S;
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), lds, s, p);
   if (p.R)
-    hipLaunchKernelGGL(moe_orth_fixup_kernel<TS>, dim3((unsigned)(p.R * (TS / 16))), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((moe_orth_fixup_kernel<TS, SYM>), dim3((unsigned)(p.R * (TS / 16))), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
 // Tile size, and which tiles are cut along K (E matrices; ctas CUs).
-template <bool KA, bool KB>
+template <bool KA, bool KB, bool SYM>
 hipError_t launch_product(OrthProduct p, int E, int ctas, hipStream_t s) {
   auto tiles = [&](int ts) {
     p.tm = (p.M + ts - 1) / ts;
     p.tn = (p.N + ts - 1) / ts;
-    p.per = p.sym ? p.tm * (p.tm + 1) / 2 : p.tm * p.tn;
+    p.per = SYM ? p.tm * (p.tm + 1) / 2 : p.tm * p.tn;
     return (int64_t)E * p.per;
   };
   // half the chip's CUs with 256 x 256 tiles, or smaller ones that reach more CUs
@@ -560,7 +586,7 @@ hipError_t launch_product(OrthProduct p, int E, int ctas, hipStream_t s) {
   p.n_dp = V - R;
   p.R = (int)R;
   p.S = (int)S;
-  return ts == 256 ? launch_tiles<256, KA, KB>(p, s) : launch_tiles<128, KA, KB>(p, s);
+  return ts == 256 ? launch_tiles<256, KA, KB, SYM>(p, s) : launch_tiles<128, KA, KB, SYM>(p, s);
 }
 
 }  // namespace
@@ -597,8 +623,8 @@ hipError_t launch_orthogonalize(int E, int M, int N, const OrthPlan& plan, const
     gram.partial = reinterpret_cast<float*>(w + plan.off_partial);
     gram.d0 = P;
     gram.alpha = kSP / (S * S);
-    e = plan.tall ? launch_product<true, true>(gram, E, ctas, st)
-                  : launch_product<false, false>(gram, E, ctas, st);
+    e = plan.tall ? launch_product<true, true, true>(gram, E, ctas, st)
+                  : launch_product<false, false, true>(gram, E, ctas, st);
     OrthProduct poly = gram;
     poly.A = poly.B = P;
     poly.sA = poly.sB = (int64_t)m * m;
@@ -607,7 +633,7 @@ hipError_t launch_orthogonalize(int E, int M, int N, const OrthPlan& plan, const
     poly.alpha = kC / kSP;
     poly.c0 = P;
     poly.beta = kB;
-    if (e == hipSuccess) e = launch_product<false, false>(poly, E, ctas, st);
+    if (e == hipSuccess) e = launch_product<false, false, true>(poly, E, ctas, st);
     OrthProduct step = poly;
     step.sym = 0;
     step.M = M;
@@ -628,8 +654,8 @@ hipError_t launch_orthogonalize(int E, int M, int N, const OrthPlan& plan, const
     step.beta = kA;
     step.gamma = 1.f / S;
     if (e == hipSuccess)
-      e = plan.tall ? launch_product<false, false>(step, E, ctas, st)
-                    : launch_product<false, true>(step, E, ctas, st);
+      e = plan.tall ? launch_product<false, false, false>(step, E, ctas, st)
+                    : launch_product<false, true, false>(step, E, ctas, st);
   }
   return e;
 }

@@ -418,9 +418,10 @@ int moe_grouped_gemm_wgrad(const moe_gemm_shape* shape, const void* dy, const vo
  *   y        [T, N], fp32 or bf16 (out_dtype)
  *   xa       fp32 [T, r] out, or NULL: A[a] x[t] before the scale (zero rows without
  *            an adapter), which moe_lora_backward takes
- * A[a] x is summed in fp32 and enters the second product as two bf16 parts (16 bits
- * of it); everything else as the layer's products.  Adapters no row names are not
- * read, and an adapter's values reach the rows that name it only.
+ * A[a] x is summed in fp32 and enters the second product in bf16 parts that hold 16
+ * (bf16 y) or 24 bits of it (fp32 y); everything else as the layer's products.
+ * Adapters no row names are not read, and an adapter's values, infinities and NaN
+ * among them, reach the rows that name it only.
  * Limits: 0 <= T, 1 <= L <= 65536, 8 <= r <= 128, D, N and r multiples of 8,
  * N * D * 2 < 2^31, 288 * 4 * max(N, D) < 2^31, T <= 2^24,
  * (T / 256 + 1) (max(N, D) / 64 + 1) < 2^23.
@@ -456,8 +457,9 @@ int moe_lora_forward(const moe_lora_shape* shape, const moe_lora_tensors* t, voi
  *   dy  bf16 [T, N];  xa fp32 [T, r] as the forward wrote it
  *   dx  [T, D] (out_dtype), da fp32 [L, r, D], db fp32 [L, N, r], all overwritten;
  *       adapters no row names get zeros (also for T == 0)
- * Limits as the forward's, and L <= 256, T * max(N, D) * 2 < 2^31, T * r * 4 < 2^31.  u and xa enter their products as two
- * bf16 parts.  Fixed summation order: bitwise reproducible.
+ * Limits as the forward's, and L <= 256, T * max(N, D) * 2 < 2^31, T * r * 6 < 2^31.
+ * u and xa enter their products in bf16 parts that hold 24 bits (16 for a bf16 dx).
+ * Fixed summation order: bitwise reproducible.
  */
 typedef struct moe_lora_grads {
   void* dx;  /* [T, D] */

@@ -133,7 +133,7 @@ hipError_t launch(bool gate_up, const GroupedGemm& g, hipStream_t s) {
 // ------------------------------------------------------------ weight gradients
 __global__ __launch_bounds__(256) void moe_gemm_wgrad_kernel(WgradGemm p) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  wgrad_whole_tile<false>(p, blockIdx.x, lds);
+  wgrad_whole_tile<false>(p, blockIdx.x, lds, NoHook{});
 }
 
 // The same products when every group has at most 64 rows (a token picks an

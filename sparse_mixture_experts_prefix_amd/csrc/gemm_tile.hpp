@@ -1276,8 +1276,13 @@ __device__ __forceinline__ void zero_acc(f32x16 (&acc)[4][4]) {
 // K-major (the rows are the reduction): both operands through the
 // transposing LDS reads, the loads written out (see lds_dma16).  A group with
 // no rows stores zeros.
-template <bool NT, class P>
-__device__ __forceinline__ void wgrad_whole_tile(const P& p, int64_t t, char* lds) {
+// Before: runs between the K loop and the stores, after: behind the stores.
+struct NoHook {
+  __device__ __forceinline__ int before() const { return 0; }
+  __device__ __forceinline__ void after(int) const {}
+};
+template <bool NT, class Hook, class P>
+__device__ __forceinline__ void wgrad_whole_tile(const P& p, int64_t t, char* lds, const Hook& hook) {
   const WgradTile w = wgrad_tile(p, t);
   if (!w.valid) return;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -1315,7 +1320,9 @@ __device__ __forceinline__ void wgrad_whole_tile(const P& p, int64_t t, char* ld
     k_loop<false, 4, false, decltype(issue_a), decltype(issue_b), true, true>(
         lds, 0, (w.K + BK - 1) / BK, wm, wn, false, lane, issue_a, issue_b, acc);
   }
+  const int h = hook.before();
   wgrad_store<NT>(w, wm, wn, lane, acc);
+  hook.after(h);
 }
 
 }  // namespace

@@ -8,7 +8,7 @@
 // stores overlap the other's loads and products.  Up to a few hundred rows the time
 // is the gradient's stores (4 G N K bytes).  They are non-temporal (nothing of a
 // gradient this size stays in a cache: 541 -> 449 us for 64 x 2048 x 4096 at 156 rows
-// each, 5.1 TB/s), and the tiles go in row order, so that what the chip stores
+// each, held in a cache), and the tiles go in row order, so that what the chip stores
 // at a time is whole rows (an eighth of the tiles per XCD instead: 602 us).
 #include "gemm_tile.hpp"
 #include "ops_launch.hpp"
@@ -17,9 +17,32 @@
 namespace moe {
 namespace {
 
+constexpr int kAhead = 256;  // tiles that run at once
+// Reads one word of each line of a share of the rows that the tiles one round ahead
+// will load (tile t + ahead: its group's lines, dealt to that group's tiles), between a
+// tile's products and its stores.  The stores keep the memory's queues full, and a
+// group's first read behind them took several microseconds of every tile.
+struct TouchAhead {
+  const RaggedWgrad& p;
+  int64_t t;
+  __device__ __forceinline__ int before() const {
+    const int64_t per = p.tiles_m * p.tiles_n;
+    const int g = (int)(t / per);
+    if (g >= p.E) return 0;
+    const int64_t rows = group_rows(p, g), first = group_first(p, g);
+    const int64_t la = (rows * p.lda + 63) / 64, lb = (rows * p.ldb + 63) / 64;  // 128-byte lines
+    const uint16_t *A = p.A + first * p.lda, *B = p.B + first * p.ldb;
+    int x = 0;
+    for (int64_t i = (t - g * per) * 256 + threadIdx.x; i < la + lb; i += per * 256)
+      x ^= i < la ? A[i * 64] : B[(i - la) * 64];
+    return x;
+  }
+  __device__ __forceinline__ void after(int x) const { asm volatile("" ::"v"(x)); }
+};
+
 __global__ __launch_bounds__(256) void moe_grouped_wgrad_kernel(RaggedWgrad p) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  wgrad_whole_tile<true>(p, blockIdx.x, lds);
+  wgrad_whole_tile<true>(p, blockIdx.x, lds, TouchAhead{p, (int64_t)blockIdx.x + kAhead});
 }
 
 // 128 x 128 tiles: 4 waves of 64 x 64 (2 x 2 MFMA blocks), two K stages of 64 rows.

@@ -54,12 +54,13 @@ hipError_t launch_lora_forward(const moe_lora_shape& s, const LoraPlan& p, const
                    static_cast<const bf16_t*>(t.lora_a), static_cast<const bf16_t*>(t.lora_b), t.adapter,
                    t.scale, s.T, s.D, s.N, s.L, s.r, y, s.out_dtype == MOE_DTYPE_BF16};
   if (p.parts)
-    return launch_lora_decode(c, false, ShrinkOut{xa, nullptr, nullptr, nullptr}, LoraLists{},
+    return launch_lora_decode(c, false, ShrinkOut{xa, nullptr, 0, nullptr, nullptr}, LoraLists{},
                               at<float>(ws, p.off_v), p.v_parts, at<float>(ws, p.off_partial), p.parts, st);
   uint16_t* parts = at<uint16_t>(ws, p.off_v16);
-  const hipError_t e = launch_shrink_rank<false>(c, ShrinkOut{xa, parts, nullptr, nullptr}, LoraLists{}, st);
+  const int np = c.out16 ? kParts16 : kParts32;
+  const hipError_t e = launch_shrink_rank<false>(c, ShrinkOut{xa, parts, np, nullptr, nullptr}, LoraLists{}, st);
   if (e != hipSuccess) return e;
-  return launch_lora_prefill(c, false, parts, p.split ? at<float>(ws, p.off_partial) : nullptr, st);
+  return launch_lora_prefill(c, false, parts, np, np, p.split ? at<float>(ws, p.off_partial) : nullptr, st);
 }
 
 hipError_t launch_lora_backward(const moe_lora_shape& s, const LoraBwdPlan& p,
@@ -76,11 +77,12 @@ hipError_t launch_lora_backward(const moe_lora_shape& s, const LoraBwdPlan& p,
   float* partial = at<float>(ws, p.off_partial);
   hipError_t e;
   if (p.parts) {
-    e = launch_lora_decode(c, true, ShrinkOut{nullptr, u16, xa, xa16}, rows, at<float>(ws, p.off_v), p.v_parts,
+    e = launch_lora_decode(c, true, ShrinkOut{nullptr, u16, kParts32, xa, xa16}, rows, at<float>(ws, p.off_v), p.v_parts,
                            partial, p.parts, st);
   } else {
-    e = launch_shrink_rank<true>(c, ShrinkOut{nullptr, u16, xa, xa16}, rows, st);
-    if (e == hipSuccess) e = launch_lora_prefill(c, true, u16, p.split ? partial : nullptr, st);
+    e = launch_shrink_rank<true>(c, ShrinkOut{nullptr, u16, kParts32, xa, xa16}, rows, st);
+    if (e == hipSuccess) e = launch_lora_prefill(c, true, u16, kParts32, c.out16 ? kParts16 : kParts32,
+                                                   p.split ? partial : nullptr, st);
   }
   if (e != hipSuccess) return e;
   return launch_lora_wgrad(rows, t.x, dy, u16, xa16, t.scale, s.T, s.D, s.N, s.L, s.r, g.da, g.db, st);

@@ -27,9 +27,10 @@ struct LoraLists {
 // Outputs of the first product; each but one may be NULL.
 struct ShrinkOut {
   float* v;           // fp32 [T][r], unscaled (zero rows without an adapter)
-  uint16_t* parts;    // bf16 [T][2 r]: scaled, upper parts then lower parts
+  uint16_t* parts;    // bf16 [T][np][r]: scaled, in np parts
+  int np;
   const float* xa;    // fp32 [T][r] in ...
-  uint16_t* xa_parts; // ... and its parts (all rows), written on the way
+  uint16_t* xa_parts; // ... and its kParts32 parts (all rows), written on the way
 };
 
 // the row's adapter, or -1
@@ -41,11 +42,18 @@ __device__ __forceinline__ float lora_scale(const LoraCall& c, int l) {
   return c.scale ? c.scale[l] : 1.f;
 }
 
-// v as two bf16 parts: hi carries 8 bits of it, lo the next 8 (v = hi + lo to 2^-16)
-__device__ __forceinline__ void split_bf16(float v, bf16_t& hi, bf16_t& lo) {
-  hi = f32_to_bf16(v);
-  lo = f32_to_bf16(v - bf16_to_f32(hi));
+// v as NP bf16 parts of 8 bits each, upper first: v = their sum to 2^-16 (two parts) or
+// 2^-24 (three), stored `step` elements apart.
+__device__ __forceinline__ void split_bf16(float v, int np, bf16_t* at, int step) {
+  for (int q = 0; q < np; ++q) {
+    const bf16_t part = f32_to_bf16(v);
+    at[q * step] = part;
+    v -= bf16_to_f32(part);
+  }
 }
+// Parts of a factor whose product is returned in bf16 (2^-16 is 1/128 of its half step),
+// and in fp32.
+constexpr int kParts16 = 2, kParts32 = 3;
 
 // 16-byte buffer loads with out-of-range offsets reading as zero
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t lora_rsrc(const void* base, uint32_t bytes) {

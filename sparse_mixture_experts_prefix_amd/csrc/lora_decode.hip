@@ -187,7 +187,7 @@ __device__ __forceinline__ void keep_v(const LoraCall& c, const ShrinkOut& o, co
   if (o.v) o.v[(int64_t)t * c.r + j] = v;
   if (o.parts) {
     const float s = l >= 0 ? v * lora_scale(c, l) : 0.f;
-    split_bf16(s, o.parts[(int64_t)t * 2 * c.r + j], o.parts[(int64_t)t * 2 * c.r + c.r + j]);
+    split_bf16(s, o.np, o.parts + (int64_t)t * o.np * c.r + j, c.r);
   }
 }
 

@@ -1,6 +1,6 @@
 // The adapters' large products (many rows): out = in W^T (or in W, W read
 // K-major) on the 256 x 256 x 64 tiles of gemm_tile.hpp, with the adapters'
-// second product, v[t] (two bf16 parts) times expand[a], added to the tile's
+// second product, v[t] (in bf16 parts) times expand[a], added to the tile's
 // accumulators in registers before they are stored.
 #include "gemm_tile.hpp"
 #include "lora.hpp"
@@ -30,7 +30,8 @@ struct LoraGemm {
   int ctas;
   float* partial;
   LoraCall call;
-  const uint16_t* parts;  // [T][2 r]
+  const uint16_t* parts;  // [T][np][r], the upper `used` parts count
+  int np, used;
 };
 __device__ __forceinline__ int group_rows(const LoraGemm& p, int) { return p.call.T; }
 __device__ __forceinline__ int group_first(const LoraGemm&, int) { return 0; }
@@ -45,9 +46,9 @@ __device__ __forceinline__ bf16x8 finite8(bf16x8 v) {
 }
 
 // acc += parts[rows] . expand[a]^T for every adapter a that the tile's rows
-// name.  Per adapter and 64 of the 2 r part columns: its rows of `parts` (the
-// other rows read as zero) and the tile's columns of expand[a] (rank j for part
-// columns j and r + j) go through LDS in the K loop's layouts and are
+// name.  Per adapter and 64 of its part columns: its rows of `parts` (the other
+// rows read as zero) and the tile's columns of expand[a] (rank j for column j of
+// every part) go through LDS in the K loop's layouts and are
 // multiplied onto the tile's sums.  Adapter values enter as finite numbers, so
 // they reach no row that does not name the adapter; adding only its rows of
 // a product held apart made the 256 sums spill.  A request's rows are
@@ -63,7 +64,7 @@ __device__ __forceinline__ void lora_expand(const LoraGemm& p, char* lds, int64_
   char* la = lds;
   char* lb = lds + kABytes;
   int* ids = reinterpret_cast<int*>(lds + kABytes + kBBytes);  // adapter of each tile row
-  const int r = c.r, r2 = 2 * r, N = c.N;
+  const int r = c.r, ld = p.np * r, rk = p.used * r, N = c.N;  // a row's part columns, and those used
   __syncthreads();  // every wave has left the K loop's stages
   ids[tid] = tid < valid ? lora_id(c, row0 + tid) : -1;
   __syncthreads();
@@ -75,7 +76,8 @@ __device__ __forceinline__ void lora_expand(const LoraGemm& p, char* lds, int64_
     id[q] = ids[64 * q + lane];
     left[q] = id[q] >= 0;
   }
-  const __amdgpu_buffer_rsrc_t rsV = make_rsrc(p.parts + row0 * r2, (uint32_t)(valid * r2 * 2));
+  auto rank = [&](int k) { return k < r ? k : k < 2 * r ? k - r : k - 2 * r; };  // of part column k < 3 r
+  const __amdgpu_buffer_rsrc_t rsV = make_rsrc(p.parts + row0 * ld, (uint32_t)(valid * ld * 2));
   while (true) {
     // the next adapter, in order of its first row (the same in every wave)
     int l = -1;
@@ -88,22 +90,22 @@ __device__ __forceinline__ void lora_expand(const LoraGemm& p, char* lds, int64_
 #pragma unroll
     for (int q = 0; q < 4; ++q) left[q] = left[q] && id[q] != l;
     const __amdgpu_buffer_rsrc_t rsE = make_rsrc(c.expand + (int64_t)l * N * r, (uint32_t)(N * r * 2));
-    for (int k0 = 0; k0 < r2; k0 += 64) {
+    for (int k0 = 0; k0 < rk; k0 += 64) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int ra = (j * 4 + wave) * 8 + sub;  // row of this lane's chunk
         const int k = k0 + 8 * ((lane & 7) ^ swz(ra));
-        const bool mine = ids[ra] == l && k < r2;
-        lds_dma16(rsV, la + (j * 4 + wave) * 1024, mine ? (uint32_t)((ra * r2 + k) * 2) : kOob, 0);
+        const bool mine = ids[ra] == l && k < rk;
+        lds_dma16(rsV, la + (j * 4 + wave) * 1024, mine ? (uint32_t)((ra * ld + k) * 2) : kOob, 0);
         uint32_t off;
         if constexpr (KMAJ) {
           const int kr = 2 * (wave * 8 + j) + (lane >> 5);  // part column, and 8 columns of the tile
           const int kk = k0 + kr, n = n0 + 8 * kmaj_chunk(kr, lane & 31);
-          off = kk < r2 && n < N ? (uint32_t)(((kk < r ? kk : kk - r) * N + n) * 2) : kOob;
+          off = kk < rk && n < N ? (uint32_t)((rank(kk) * N + n) * 2) : kOob;
         } else {
           const int rb = (wave * 8 + j) * 8 + sub;
           const int kb = k0 + 8 * ((lane & 7) ^ swz(rb)), n = n0 + rb;
-          off = kb < r2 && n < N ? (uint32_t)((n * r + (kb < r ? kb : kb - r)) * 2) : kOob;
+          off = kb < rk && n < N ? (uint32_t)((n * r + rank(kb)) * 2) : kOob;
         }
         lds_dma16(rsE, lb + (wave * 8 + j) * 1024, off, 0);
       }
@@ -185,8 +187,8 @@ hipError_t launch_typed(void (*k32)(TypedLora<false>), void (*k16)(TypedLora<tru
 
 }  // namespace
 
-hipError_t launch_lora_prefill(const LoraCall& c, bool kmajor, const uint16_t* parts, float* partial,
-                               hipStream_t s) {
+hipError_t launch_lora_prefill(const LoraCall& c, bool kmajor, const uint16_t* parts, int np, int used,
+                               float* partial, hipStream_t s) {
   static std::atomic<uint64_t> done[6];
   LoraGemm p{};
   p.A = c.in;
@@ -200,6 +202,8 @@ hipError_t launch_lora_prefill(const LoraCall& c, bool kmajor, const uint16_t* p
   p.n_tiles_n = (c.N + BN - 1) / BN;
   p.call = c;
   p.parts = parts;
+  p.np = np;
+  p.used = used;
   p.partial = partial;
   hipError_t e = partial ? split_ctas(&p.ctas) : hipSuccess;
   if (e != hipSuccess) return e;

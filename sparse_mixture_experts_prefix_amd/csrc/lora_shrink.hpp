@@ -60,7 +60,7 @@ __device__ __forceinline__ void lora_shrink_tile(const LoraCall& c, const Shrink
     for (int e = threadIdx.x; e < rows * c.r; e += blockDim.x) {
       const int64_t t = t0 + e / c.r;
       const int j = e % c.r;
-      split_bf16(o.xa[t * c.r + j], o.xa_parts[t * 2 * c.r + j], o.xa_parts[t * 2 * c.r + c.r + j]);
+      split_bf16(o.xa[t * c.r + j], kParts32, o.xa_parts + t * kParts32 * c.r + j, c.r);
     }
   }
   // distinct adapters: bit `row` of `left` is a row whose adapter is yet to come
@@ -169,12 +169,7 @@ __device__ __forceinline__ void lora_shrink_tile(const LoraCall& c, const Shrink
           if (PART || o.v) o.v[t * c.r + j] = acc[b][i];
           if constexpr (PART) continue;
           const float v = acc[b][i] * sc;
-          if (o.parts) {
-            bf16_t hi, lo;
-            split_bf16(v, hi, lo);
-            o.parts[t * 2 * c.r + j] = hi;
-            o.parts[t * 2 * c.r + c.r + j] = lo;
-          }
+          if (o.parts) split_bf16(v, o.np, o.parts + t * o.np * c.r + j, c.r);
         }
       }
     }

@@ -3,7 +3,7 @@
 //   db[l][n][j] = scale[l] sum over l's rows of xa[t][j] dy[t][n]
 // One workgroup owns 128 columns (of x or dy) of one adapter and walks its
 // rows in stages of 64: the rows' values (gathered, each row's 256 bytes) and
-// their two bf16 parts of u or xa go through a ring of LDS stages, and both
+// their three bf16 parts of u or xa go through a ring of LDS stages, and both
 // operands are read transposed, the rows being the reduction.  MFMA 16x16x32,
 // 16 ranks x 32 columns per wave.  Row numbers come through LDS too, 1024 at a
 // time, so the loop has no load that it waits for out of turn.  Bound by reading
@@ -18,7 +18,7 @@ namespace {
 struct LoraWgrad {
   LoraLists rows;
   const uint16_t* z[2];    // x [T][D], dy [T][N]
-  const uint16_t* v[2];    // parts of u and of xa [T][2 r]
+  const uint16_t* v[2];    // parts of u and of xa [T][3][r]
   float* out[2];           // da, db
   int width[2];            // D, N
   const float* scale;      // [L] or NULL
@@ -29,9 +29,12 @@ struct LoraWgrad {
 constexpr int kWgCols = 128;
 constexpr int kWgZ = 64 * kWgCols * 2;  // 16 KB: a stage's rows
 constexpr int kWgIds = 1024;            // row numbers held at a time
-// A stage's parts: each wave's 16 rows of 4 r bytes in RB KB of its own.
-template <int RB> constexpr int wg_stage_bytes() { return kWgZ + 4 * RB * 1024; }
-template <int RB> constexpr int wg_stages() { return RB == 1 ? 3 : RB == 8 ? 3 : 2; }
+constexpr int kNP = kParts32;
+// A stage's parts: each wave's 16 rows of 6 r bytes in wg_v() KB of its own.
+template <int RB> constexpr int wg_v() { return (16 * 2 * kNP * 16 * RB + 1023) / 1024; }
+template <int RB> constexpr int wg_stage_bytes() { return kWgZ + 4 * wg_v<RB>() * 1024; }
+// (two workgroups per CU up to rank 32)
+template <int RB> constexpr int wg_stages() { return RB == 1 || RB == 4 ? 3 : 2; }
 template <int RB> constexpr int wg_lds_bytes() { return wg_stages<RB>() * wg_stage_bytes<RB>() + kWgIds * 4; }
 
 // 16-byte chunk c of a stage's row (16 chunks of 8 columns) sits at c ^ wg_swz(row):
@@ -42,7 +45,7 @@ __device__ __forceinline__ int wg_swz(int row) { return 2 * (row & 3) + 8 * ((ro
 template <int RB>
 __global__ __launch_bounds__(256) void moe_lora_wgrad_kernel(LoraWgrad p) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  constexpr int S = wg_stages<RB>(), SB = wg_stage_bytes<RB>(), V = 4 + RB;
+  constexpr int S = wg_stages<RB>(), SB = wg_stage_bytes<RB>(), NV = wg_v<RB>(), V = 4 + NV;
   int* ids = reinterpret_cast<int*>(lds + S * SB);
   const int l = blockIdx.y;
   const int which = blockIdx.x >= p.tiles0;
@@ -51,7 +54,7 @@ __global__ __launch_bounds__(256) void moe_lora_wgrad_kernel(LoraWgrad p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, gq = lane >> 4;
-  const int r = p.r, rowb = 4 * r;  // bytes of a row's two parts
+  const int r = p.r, rowb = 2 * kNP * r;  // bytes of a row's parts
   const int rows = __builtin_amdgcn_readfirstlane(p.rows.counts[l]);
   const int32_t* list = p.rows.sorted + __builtin_amdgcn_readfirstlane(p.rows.offsets[l]);
   const __amdgpu_buffer_rsrc_t rsZ = make_rsrc(which ? p.z[1] : p.z[0], (uint32_t)((int64_t)p.T * C * 2));
@@ -63,7 +66,7 @@ __global__ __launch_bounds__(256) void moe_lora_wgrad_kernel(LoraWgrad p) {
     for (int j = 0; j < 2; ++j) acc[b][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // A stage's loads: wave w brings rows 16 w .. + 15.  Load i: rows 4 i + lane / 16 of
-  // them, 256 bytes each; then RB loads of their parts, 16 bytes per lane in row
+  // them, 256 bytes each; then NV loads of their parts, 16 bytes per lane in row
   // order.  Rows past the adapter's last (-1) read as zero.
   auto issue = [&](int stage, int slot) {
     char* st = lds + __builtin_amdgcn_readfirstlane(slot * SB);
@@ -77,10 +80,10 @@ __global__ __launch_bounds__(256) void moe_lora_wgrad_kernel(LoraWgrad p) {
                 t >= 0 && n < C ? (uint32_t)t * (uint32_t)(C * 2) + (uint32_t)n * 2 : kOob, 0);
     }
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
+    for (int b = 0; b < NV; ++b) {
       const int at = b * 1024 + lane * 16, q = at / rowb;
       const int t = q < 16 ? id[q & 15] : -1;
-      lds_dma16(rsV, st + kWgZ + (RB * wave + b) * 1024,
+      lds_dma16(rsV, st + kWgZ + (NV * wave + b) * 1024,
                 t >= 0 ? (uint32_t)t * (uint32_t)rowb + (uint32_t)(at % rowb) : kOob, 0);
     }
   };
@@ -119,11 +122,11 @@ __global__ __launch_bounds__(256) void moe_lora_wgrad_kernel(LoraWgrad p) {
           auto at = [&](int row) { return st + row * 256 + ((cc >> 3) ^ wg_swz(row)) * 16 + (cc & 7) * 2; };
           z[j] = read_tr(at(k), at(k + 4));
         }
-        const char* v0 = st + kWgZ + (k >> 4) * (RB * 1024) + (k & 15) * rowb + 8 * (col & 3);
+        const char* v0 = st + kWgZ + (k >> 4) * (NV * 1024) + (k & 15) * rowb + 8 * (col & 3);
 #pragma unroll
         for (int b = 0; b < RB; ++b)
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
+          for (int part = 0; part < kNP; ++part) {
             // (ranks past r read the neighbour's values: they reach results that are not stored)
             const char* at = v0 + part * 2 * r + 32 * b;
             const bf16x8 v = read_tr(at, at + 4 * rowb);

@@ -23,10 +23,11 @@ hipError_t launch_lora_backward(const moe_lora_shape& s, const LoraBwdPlan& p,
                                 const moe_lora_tensors& t, const void* dy, const float* xa,
                                 const moe_lora_grads& g, void* ws, hipStream_t st);
 // out = in w^T + the adapters' second product (kmajor: w and the adapters as the
-// backward pass reads them).  Many rows: parts16 holds the first product's two
-// bf16 parts; partial (or NULL: no cut along K) room for partial tiles.
-hipError_t launch_lora_prefill(const LoraCall& c, bool kmajor, const uint16_t* parts16, float* partial,
-                               hipStream_t s);
+// backward pass reads them).  Many rows: parts16 [T][np][r] holds the first product's
+// bf16 parts, of which the upper `used` count; partial (or NULL: no cut along K) room
+// for partial tiles.
+hipError_t launch_lora_prefill(const LoraCall& c, bool kmajor, const uint16_t* parts16, int np, int used,
+                               float* partial, hipStream_t s);
 // At most 64 rows, both products; rows.counts set: the rows' lists too.  Workspace:
 // v fp32 [v_parts][T][r], partial fp32 [parts][T][N].
 hipError_t launch_lora_decode(const LoraCall& c, bool kmajor, const ShrinkOut& o, const LoraLists& rows,

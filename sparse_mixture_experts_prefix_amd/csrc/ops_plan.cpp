@@ -127,7 +127,7 @@ int make_lora_plan(const moe_lora_shape* s, LoraPlan* p) {
   p->split = !few && may_split((s->T + 255) / 256, s->N, s->D);
   Layout l;
   p->off_v = l.take(sizeof(float) * p->v_parts * T * r);
-  p->off_v16 = l.take(few ? 0 : sizeof(uint16_t) * T * 2 * r);
+  p->off_v16 = l.take(few ? 0 : sizeof(uint16_t) * T * 3 * r);
   p->off_partial = l.take(few ? sizeof(float) * p->parts * T * s->N : p->split ? kPartialBytes : 0);
   p->total = l.o;
   return MOE_OK;
@@ -139,7 +139,7 @@ int make_lora_backward_plan(const moe_lora_shape* s, LoraBwdPlan* p) {
   if (s->L > kLoraMaxTrained) return MOE_ERR_UNSUPPORTED;
   // gathered rows are addressed with 32-bit byte offsets
   const int64_t w = s->N > s->D ? s->N : s->D;
-  if (s->T * w * 2 >= kLim31 || (int64_t)s->T * s->r * 4 >= kLim31) return MOE_ERR_UNSUPPORTED;
+  if (s->T * w * 2 >= kLim31 || (int64_t)s->T * s->r * 6 >= kLim31) return MOE_ERR_UNSUPPORTED;
   const size_t T = s->T, r = s->r;
   const bool few = s->T <= kLoraFewRows;
   p->parts = few ? few_row_parts(s->D, s->N) : 0;
@@ -147,8 +147,8 @@ int make_lora_backward_plan(const moe_lora_shape* s, LoraBwdPlan* p) {
   p->split = !few && may_split((s->T + 255) / 256, s->D, s->N);
   Layout l;
   p->off_v = l.take(sizeof(float) * p->v_parts * T * r);
-  p->off_u16 = l.take(sizeof(uint16_t) * T * 2 * r);
-  p->off_xa16 = l.take(sizeof(uint16_t) * T * 2 * r);
+  p->off_u16 = l.take(sizeof(uint16_t) * T * 3 * r);
+  p->off_xa16 = l.take(sizeof(uint16_t) * T * 3 * r);
   p->off_rows = l.take(sizeof(int32_t) * (2 * s->L + T));
   p->off_partial = l.take(few ? sizeof(float) * p->parts * T * s->D : p->split ? kPartialBytes : 0);
   p->total = l.o;

@@ -40,7 +40,7 @@ struct LoraPlan {
   int v_parts;         // ... and for the first product
   int split;           // 256-row tiles: the last round may be cut along K
   size_t off_v;        // few rows: fp32 [v_parts][T][r], A x in parts
-  size_t off_v16;      // many rows: bf16 [T][2 r], its two parts
+  size_t off_v16;      // many rows: bf16 [T][3][r], its bf16 parts (two of them for a bf16 y)
   size_t off_partial;  // fp32 [parts][T][N], or partial tiles
   size_t total;
 };
@@ -49,8 +49,8 @@ int make_lora_plan(const moe_lora_shape* s, LoraPlan* p);
 struct LoraBwdPlan {
   int parts, v_parts, split;  // as above, for dx and u
   size_t off_v;        // few rows: fp32 [v_parts][T][r], B^T dy in parts
-  size_t off_u16;      // bf16 [T][2 r]: u's two parts
-  size_t off_xa16;     // bf16 [T][2 r]: xa's
+  size_t off_u16;      // bf16 [T][3][r]: u's parts
+  size_t off_xa16;     // bf16 [T][3][r]: xa's
   size_t off_rows;     // int32 [2 L + T]: the adapters' rows (LoraLists)
   size_t off_partial;  // fp32 [parts][T][D], or partial tiles
   size_t total;

@@ -11,33 +11,44 @@
 namespace moe {
 namespace {
 
-// Workgroups: the rows' lists (one per adapter, when asked for), then the tiles.
+// Workgroups (x): the rows' lists (one per adapter, when asked for), then the tiles;
+// y: groups of 16 RB ranks; z: slots of a tile's distinct adapters.
 template <int RB, bool KMAJ>
 __global__ __launch_bounds__(256) void moe_lora_shrink_kernel(LoraCall c, ShrinkOut o, LoraLists rows) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int lists = rows.counts ? c.L : 0;
-  if ((int)blockIdx.x < lists)
+  if ((int)blockIdx.x >= lists)
+    lora_shrink_tile<RB, KMAJ, false>(c, o, blockIdx.x - lists, blockIdx.y * RB, blockIdx.z, gridDim.z, 0,
+                                      (c.K + 63) / 64, lds);
+  else if (blockIdx.y == 0 && blockIdx.z == 0)
     lora_list(c, rows, blockIdx.x, reinterpret_cast<int*>(lds));
-  else
-    lora_shrink_tile<RB, KMAJ, false>(c, o, blockIdx.x - lists, 0, 0, 1, 0, (c.K + 63) / 64, lds);
 }
 
 template <int RB, bool KMAJ>
 hipError_t launch_shrink(const LoraCall& c, const ShrinkOut& o, const LoraLists& rows, hipStream_t s) {
   static std::atomic<uint64_t> done;
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(moe_lora_shrink_kernel<RB, KMAJ>),
-                                 shrink_lds_bytes<RB>(), done);
+  const hipError_t e =
+      allow_lds(reinterpret_cast<const void*>(moe_lora_shrink_kernel<RB, KMAJ>), shrink_lds_bytes<RB>(), done);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_lora_shrink_kernel<RB, KMAJ>), dim3((unsigned)((c.T + 15) / 16 + (rows.counts ? c.L : 0))),
-                     dim3(256), shrink_lds_bytes<RB>(), s, c, o, rows);
+  const int tiles = (c.T + 15) / 16, groups = (c.r + 16 * RB - 1) / (16 * RB);
+  // up to 16 adapters per tile at once while that keeps the grid at a few rounds
+  // (slots without an adapter end at once)
+  int slots = 1;
+  while (slots < 16 && tiles * groups * slots < 1024) slots *= 2;
+  const dim3 grid((unsigned)(tiles + (rows.counts ? c.L : 0)), (unsigned)groups, (unsigned)slots);
+  hipLaunchKernelGGL((moe_lora_shrink_kernel<RB, KMAJ>), grid, dim3(256), shrink_lds_bytes<RB>(), s, c, o, rows);
   return hipGetLastError();
 }
 
+// All ranks in one workgroup (the rows are read once), or fewer where the tiles alone
+// would leave CUs idle.
 template <bool KMAJ>
 hipError_t launch_shrink_rank(const LoraCall& c, const ShrinkOut& o, const LoraLists& rows, hipStream_t s) {
-  if (c.r <= 16) return launch_shrink<1, KMAJ>(c, o, rows, s);
-  if (c.r <= 32) return launch_shrink<2, KMAJ>(c, o, rows, s);
-  if (c.r <= 64) return launch_shrink<4, KMAJ>(c, o, rows, s);
+  int rb = c.r <= 16 ? 1 : c.r <= 32 ? 2 : c.r <= 64 ? 4 : 8;
+  while (rb > 1 && (c.T + 15) / 16 * ((c.r + 16 * rb - 1) / (16 * rb)) < 256) rb /= 2;
+  if (rb == 1) return launch_shrink<1, KMAJ>(c, o, rows, s);
+  if (rb == 2) return launch_shrink<2, KMAJ>(c, o, rows, s);
+  if (rb == 4) return launch_shrink<4, KMAJ>(c, o, rows, s);
   return launch_shrink<8, KMAJ>(c, o, rows, s);
 }
 

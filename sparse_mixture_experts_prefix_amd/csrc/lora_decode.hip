@@ -1,11 +1,12 @@
-// The adapters' products for few rows (at most 64): two launches.
+// The adapters' products for few rows (lora_few_rows in ops_plan.hpp): two launches.
 //
-// First, in one launch: the projection's weights are streamed once (tiles of all
-// rows x 64 columns, K cut into parts so that the grid fills the chip, fp32
-// partial sums), while other workgroups compute the adapters' first product
-// (and, for the backward pass, the rows' lists).  Then each output is its
-// partial sums, in part order, plus its row's second product in fp32.  Bound by
-// streaming W (2 N K bytes) and the live adapters.
+// First, in one launch: the projection's weights are streamed once (tiles of up to 64
+// rows x 64 columns, K cut into parts so that the grid fills the chip, fp32 partial
+// sums; more rows take several tiles, which share the weights in an XCD's L2), while
+// other workgroups compute the adapters' first product (and, for the backward pass,
+// the rows' lists).  Then each output is its partial sums, in part order, plus its
+// row's second product in fp32.  Bound by streaming W (2 N K bytes) and the live
+// adapters.
 #include "lora_rows.hpp"
 #include "lora_shrink.hpp"
 #include "ops_launch.hpp"
@@ -14,8 +15,8 @@
 namespace moe {
 namespace {
 
-// Projection tile: T <= 16 MT rows x 64 columns, chunks q0 .. q1 - 1 of 64 k.  A
-// stage (all rows, 64 columns) is shared by the four waves, 16 columns each, in a
+// Projection tile: `rows` <= 16 MT rows from t0 on x 64 columns, chunks q0 .. q1 - 1 of
+// 64 k.  A stage (all rows, 64 columns) is shared by the four waves, 16 columns each, in a
 // ring of four (64 rows) or six stages, all but one in flight, one barrier per stage.  64
 // or 72 KB of LDS per workgroup, so two share a CU (each wave with its own ring of whole
 // stages took 128 KB at 64 rows: one workgroup per CU, 24 us against 15 us for
@@ -32,7 +33,8 @@ __device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int col_swz(int r) { return 2 * ((r >> 1) & 1) + 4 * ((r >> 3) & 1); }
 
 template <int MT, bool KMAJ>
-__device__ __forceinline__ void project_tile(const LoraCall& c, int n0, int q0, int q1, float* out, char* lds) {
+__device__ __forceinline__ void project_tile(const LoraCall& c, int t0, int rows, int n0, int q0, int q1, float* out,
+                                             char* lds) {
   constexpr int SB = tile_stage_bytes<MT>(), AB = MT * 2048, S = tile_stages<MT>();
   constexpr int LA = MT * 2;            // 1-KB blocks of rows
   constexpr int V = SB / 4096;          // loads per wave and stage
@@ -40,7 +42,7 @@ __device__ __forceinline__ void project_tile(const LoraCall& c, int n0, int q0, 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, gq = lane >> 4, ir = lane >> 3, ip = lane & 7;
   const int K = c.K, N = c.N;
-  const __amdgpu_buffer_rsrc_t rsA = lora_rsrc(c.in, (uint32_t)(c.T * K * 2));
+  const __amdgpu_buffer_rsrc_t rsA = lora_rsrc(c.in + (int64_t)t0 * K, (uint32_t)(rows * K * 2));
   const __amdgpu_buffer_rsrc_t rsB = lora_rsrc(c.w, (uint32_t)((int64_t)N * K * 2));
   // block b of a stage: rows 8 b + ir (b < LA), else weight rows (or k-rows) 8 (b - LA) + ir
   auto issue = [&](int q, int slot) {
@@ -51,7 +53,7 @@ __device__ __forceinline__ void project_tile(const LoraCall& c, int n0, int q0, 
       const int b = wave + 4 * i;  // uniform
       if (b < LA) {
         const int r = 8 * b + ir, k = k0 + 8 * (ip ^ row_swz(r));
-        lds_dma16(rsA, st + b * 1024, r < c.T && k < K ? (uint32_t)((r * K + k) * 2) : kShrinkOob, 0);
+        lds_dma16(rsA, st + b * 1024, r < rows && k < K ? (uint32_t)((r * K + k) * 2) : kShrinkOob, 0);
       } else if (b < LA + 8) {
         const int r = 8 * (b - LA) + ir;
         uint32_t off;
@@ -125,13 +127,14 @@ __device__ __forceinline__ void project_tile(const LoraCall& c, int n0, int q0, 
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * i + 4 * gq + r;
-      if (t < c.T) out[(int64_t)t * N + cn] = acc[i][r];
+      if (t < rows) out[(int64_t)(t0 + t) * N + cn] = acc[i][r];
     }
 }
 
 struct FewRows {
   int shrink, lists;  // workgroups of the first product, and of the rows' lists
   int tiles, parts;   // column tiles, parts of K
+  int blocks;         // blocks of 64 rows
   int v_parts;        // parts of K of the first product
   float* v;           // [v_parts][T][r]
   float* partial;     // [parts][T][N]
@@ -160,8 +163,11 @@ __global__ __launch_bounds__(256) void moe_lora_decode_kernel(LoraCall c, Shrink
     return;
   }
   b -= f.lists;
-  const int part = b / f.tiles, nq = (c.K + 63) / 64;
-  project_tile<MT, KMAJ>(c, (b % f.tiles) * 64, (int)((int64_t)part * nq / f.parts),
+  // eight column tiles side by side (one per XCD), their row blocks behind them
+  const int per = (f.tiles + 7) / 8 * 8 * f.blocks, part = b / per, u = b % per / 8;
+  const int tile = u / f.blocks * 8 + b % 8, t0 = u % f.blocks * 64, nq = (c.K + 63) / 64;
+  if (tile >= f.tiles) return;
+  project_tile<MT, KMAJ>(c, t0, min(64, c.T - t0), tile * 64, (int)((int64_t)part * nq / f.parts),
                          (int)((int64_t)(part + 1) * nq / f.parts),
                          f.partial + (int64_t)part * c.T * c.N, lds);
 }
@@ -277,7 +283,7 @@ hipError_t launch(const LoraCall& c, const ShrinkOut& o, const LoraLists& rows, 
   constexpr int lds = tile_lds_bytes<MT>() > shrink_lds_bytes<1>() ? tile_lds_bytes<MT>() : shrink_lds_bytes<1>();
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(moe_lora_decode_kernel<MT, KMAJ>), lds, done);
   if (e != hipSuccess) return e;
-  const int64_t blocks = f.shrink + f.lists + (int64_t)f.tiles * f.parts;
+  const int64_t blocks = f.shrink + f.lists + (int64_t)(f.tiles + 7) / 8 * 8 * f.blocks * f.parts;
   hipLaunchKernelGGL((moe_lora_decode_kernel<MT, KMAJ>), dim3((unsigned)blocks), dim3(256), lds, s, c, o, rows, f);
   return hipGetLastError();
 }
@@ -296,7 +302,7 @@ hipError_t launch_finish(const LoraCall& c, const ShrinkOut& o, const FewRows& f
 hipError_t launch_lora_decode(const LoraCall& c, bool kmajor, const ShrinkOut& o, const LoraLists& rows,
                               float* v, int v_parts, float* partial, int parts, hipStream_t s) {
   const FewRows f{(c.T + 15) / 16 * ((c.r + 15) / 16) * v_parts * 16, rows.counts ? c.L : 0, (c.N + 63) / 64,
-                  parts, v_parts, v, partial};
+                  parts, (c.T + 63) / 64, v_parts, v, partial};
   hipError_t e;
   if (c.T <= 16)
     e = kmajor ? launch<1, true>(c, o, rows, f, s) : launch<1, false>(c, o, rows, f, s);

@@ -103,8 +103,9 @@ namespace {
 // first product's longer waits, so that all of them run from the start (512 columns' tiles
 // and the first product's 16 workgroups beyond them: 14.8 us against 13.9 us for 16 rows x
 // 4096 x 4096), each wave with two or more of the 64-wide K chunks.
-int few_row_parts(int64_t N, int64_t K) {
-  const int64_t tiles = (N + 63) / 64, chunks = (K + 63) / 64;
+int few_row_parts(int64_t T, int64_t N, int64_t K) {
+  const int64_t blocks = T > 64 ? (T + 63) / 64 : 1;  // no rows: a plan like one row's
+  const int64_t tiles = (N + 63) / 64 * blocks, chunks = (K + 63) / 64;
   int64_t parts = 496 / tiles;
   if (parts > chunks / 8) parts = chunks / 8;
   return parts < 1 ? 1 : (int)parts;
@@ -121,8 +122,8 @@ int make_lora_plan(const moe_lora_shape* s, LoraPlan* p) {
   const int rc = check_lora_shape(s);
   if (rc) return rc;
   const size_t T = s->T, r = s->r;
-  const bool few = s->T <= kLoraFewRows;
-  p->parts = few ? few_row_parts(s->N, s->D) : 0;
+  const bool few = lora_few_rows(s);
+  p->parts = few ? few_row_parts(s->T, s->N, s->D) : 0;
   p->v_parts = few ? few_row_v_parts(s, s->D) : 0;
   p->split = !few && may_split((s->T + 255) / 256, s->N, s->D);
   Layout l;
@@ -141,8 +142,8 @@ int make_lora_backward_plan(const moe_lora_shape* s, LoraBwdPlan* p) {
   const int64_t w = s->N > s->D ? s->N : s->D;
   if (s->T * w * 2 >= kLim31 || (int64_t)s->T * s->r * 6 >= kLim31) return MOE_ERR_UNSUPPORTED;
   const size_t T = s->T, r = s->r;
-  const bool few = s->T <= kLoraFewRows;
-  p->parts = few ? few_row_parts(s->D, s->N) : 0;
+  const bool few = lora_few_rows(s);
+  p->parts = few ? few_row_parts(s->T, s->D, s->N) : 0;
   p->v_parts = few ? few_row_v_parts(s, s->N) : 0;
   p->split = !few && may_split((s->T + 255) / 256, s->D, s->N);
   Layout l;

@@ -32,8 +32,10 @@ constexpr int kLoraMaxTrained = 256;  // adapters of a backward pass (it groups 
 int check_lora_shape(const moe_lora_shape* s);
 int check_lora_tensors(const moe_lora_shape* s, const moe_lora_tensors* t);
 
-// Rows of the few-row path, which streams W with all rows in one tile.
-constexpr int kLoraFewRows = 64;
+// Whether a call takes the few-row path: its second product reads an adapter's rows
+// once per row that names it (2 N r bytes), whoever its neighbours are, where the
+// 256-row tiles take a stage of each adapter they hold.
+inline bool lora_few_rows(const moe_lora_shape* s) { return s->T <= 64 || (s->T <= 256 && s->T * s->r <= 8192); }
 
 struct LoraPlan {
   int parts;           // few rows: parts K is cut into (0: the 256-row tiles)

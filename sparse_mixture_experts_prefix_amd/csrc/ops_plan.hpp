@@ -34,8 +34,14 @@ int check_lora_tensors(const moe_lora_shape* s, const moe_lora_tensors* t);
 
 // Whether a call takes the few-row path: its second product reads an adapter's rows
 // once per row that names it (2 N r bytes), whoever its neighbours are, where the
-// 256-row tiles take a stage of each adapter they hold.
-inline bool lora_few_rows(const moe_lora_shape* s) { return s->T <= 64 || (s->T <= 256 && s->T * s->r <= 8192); }
+// 256-row tiles take a stage of each adapter they hold.  N = D = 4096, few rows against
+// tiles: 250 rows of 30 adapters, rank 64 67 us against 208, rank 128 96 against 371;
+// of 2 adapters, rank 64 54 against 52, rank 128 77 against 63; 100 rows of 2 adapters,
+// rank 128 41 against 53.  How many adapters the rows name is known on the device
+// alone: L bounds it.
+inline bool lora_few_rows(const moe_lora_shape* s) {
+  return s->T <= 64 || (s->T <= 256 && (s->L > 4 || s->T * s->r <= 16384));
+}
 
 struct LoraPlan {
   int parts;           // few rows: parts K is cut into (0: the 256-row tiles)

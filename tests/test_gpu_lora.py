@@ -89,6 +89,15 @@ def test_rows(T, kind):
     check(T, 328, 264, 5, 16, kind, seed=T)
 
 
+@pytest.mark.parametrize("T,L,r", [(65, 6, 128), (66, 2, 8), (128, 5, 64), (129, 4, 120), (193, 30, 40),
+                                   (255, 30, 128), (256, 5, 16), (256, 4, 64), (256, 4, 72)])
+@pytest.mark.parametrize("kind", ["mixed", "runs"])
+def test_more_rows_than_a_tile_of_64(T, L, r, kind):
+    """Both sides of the choice between the few rows' launches and the 256-row tiles."""
+    check(T, 1096, 264, L, r, kind, seed=r)
+    check(T, 264, 1096, L, r, kind, out=torch.float32, seed=T)
+
+
 @pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 64, 72, 128])
 @pytest.mark.parametrize("T", [9, 300])
 def test_ranks(T, r):

@@ -43,8 +43,8 @@ __global__ __launch_bounds__(256) void moe_gather_rows_kernel(const Src* __restr
 }
 
 __global__ void moe_fill_f32_kernel(float* __restrict__ out, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < n) out[i] = 0.f;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
+    out[i] = 0.f;
 }
 
 // row_assign[row_of[a]] = a
@@ -279,7 +279,8 @@ hipError_t launch_row_assign(const int32_t* row_of, int A, int64_t cap, int32_t*
 
 hipError_t launch_fill_f32(float* out, int64_t n, hipStream_t s) {
   if (n <= 0) return hipSuccess;
-  hipLaunchKernelGGL(moe_fill_f32_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, out, n);
+  const int64_t blocks = (n + 255) / 256, most = 1 << 20;  // a grid holds fewer than 2^32 threads
+  hipLaunchKernelGGL(moe_fill_f32_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, s, out, n);
   return hipGetLastError();
 }
 

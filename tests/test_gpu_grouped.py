@@ -273,3 +273,12 @@ def test_graph_replays_match_eager(rows):
         step(*e, torch.empty_like(ws), torch.empty_like(wsx))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((y, dx, dw), e)), r
+
+
+def test_no_rows_fill_more_than_a_grid_of_threads():
+    """A call without rows writes zeros over all of dw, also past 2^32 elements."""
+    G, N, K = 9, 23160, 23160
+    dw = torch.ones((G, N, K), device=DEV)
+    e = torch.empty((0, N), dtype=torch.bfloat16, device=DEV), torch.empty((0, K), dtype=torch.bfloat16, device=DEV)
+    moe.moe_grouped_gemm_wgrad(*e, torch.zeros(G + 1, dtype=torch.int32, device=DEV), dw=dw)
+    assert all(not dw[g].any() for g in range(G))

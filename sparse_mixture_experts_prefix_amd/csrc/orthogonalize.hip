@@ -5,7 +5,7 @@
 //   Q = b P + c P P           symmetric, m^3, half needed
 //   X' = a X + Q X (or X Q)   m^2 n
 // Every product runs on MFMA tiles (256 x 256 x 64 with the K loop of gemm_tile.hpp;
-// 128 x 128 x 64 where those would leave most CUs idle) in the layout X has: rows
+// 128 x 128 or 64 x 64 where those would leave most CUs idle) in the layout X has: rows
 // or columns as the reduction, so nothing is transposed.  The symmetric ones
 // compute the tiles on and below the diagonal and store each twice.
 //
@@ -251,7 +251,7 @@ template <bool SYM, int ROWS, int TS, class Fill>
 __device__ __forceinline__ void emit_tile(const OrthProduct& p, int64_t at, int m, int n, float* tile, bool mirror,
                                           Fill fill) {
   const int rows = min(ROWS, p.M - m), cols = min(TS, p.N - n);  // multiples of 8
-  constexpr int PIECES = ROWS * TS / 8 / 256;
+  constexpr int PIECES = (ROWS * TS / 8 + 255) / 256;  // (past ROWS: past `rows` too)
   Addend<SYM> a[PIECES];
   const int64_t base = at + (int64_t)m * p.N + n;
 #pragma unroll
@@ -415,15 +415,25 @@ __global__ __launch_bounds__(256) void moe_orth_tile256_kernel(OrthProduct p) {
   }
 }
 
-// 128 x 128 tiles: 4 waves of 64 x 64 (2 x 2 MFMA blocks), three K stages of 32 KB
-// in LDS, two of them in flight.  Two workgroups share a CU's registers but not its
-// LDS; taken where the 256 x 256 tiles are too few for the chip.
-constexpr int kStage128 = 2 * 128 * BK * 2;
-template <bool KA, bool KB, bool SYM>
-__global__ __launch_bounds__(256) void moe_orth_tile128_kernel(OrthProduct p) {
+// 128 x 128 or 64 x 64 tiles (TS): 4 waves of 2 x 2 or one MFMA block of 32 x 32, three
+// K stages of 32 or 16 KB in LDS, two of them in flight.  Taken where the larger tiles
+// are too few for the chip; what a launch takes then is one tile's chain of loads,
+// products and stores, which the smaller tile shortens: 7 to 12 us with TS 128, 4 to 6
+// with TS 64 for matrices of a few hundred rows and columns.
+template <int TS>
+constexpr int small_stage_bytes() { return 2 * TS * BK * 2; }
+// K-major rows of 64 columns are 128 bytes: chunk c of k-row k sits at c ^ 4 (k / 2 % 2), so
+// that the four k-rows of a transposing read hit every bank once; of 128 columns as kmaj_chunk
+template <int TS>
+__device__ __forceinline__ int small_chunk(int k, int c) {
+  return TS == 128 ? kmaj_chunk(k, c) : c ^ (4 * ((k >> 1) & 1));
+}
+template <int TS, bool KA, bool KB, bool SYM>
+__global__ __launch_bounds__(256) void moe_orth_tile_kernel(OrthProduct p) {
+  constexpr int SB = small_stage_bytes<TS>(), NB = TS / 64, CH = TS / 8;  // MFMA blocks a side; chunks of a k-row
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   OrthTile t;
-  if (!orth_tile<128>(p, blockIdx.x, t)) return;
+  if (!orth_tile<TS>(p, blockIdx.x, t)) return;
   const int lane = threadIdx.x & 63, sub = lane >> 3;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -432,16 +442,16 @@ __global__ __launch_bounds__(256) void moe_orth_tile128_kernel(OrthProduct p) {
       make_rsrc(p.A + t.e * p.sA, (uint32_t)((KA ? p.K : p.M) * p.lda * 2));
   const __amdgpu_buffer_rsrc_t rsB =
       make_rsrc(p.B + t.e * p.sB, (uint32_t)((KB ? p.K : p.N) * p.ldb * 2));
-  // a stage's operand is 16 blocks of 1 KB, four per wave: 8 rows of 128 bytes, or
-  // (K-major) 4 k-rows of 256 bytes, whose chunk c sits at c ^ 4 (k % 4) as kmaj_chunk's
+  // a stage's operand is TS / 8 blocks of 1 KB, a quarter per wave: 8 rows of 128 bytes,
+  // or (K-major) k-rows of 2 TS bytes
   auto issue_op = [&](const __amdgpu_buffer_rsrc_t rs, bool kmaj, int r0, int rows, int ld, int stage, char* st) {
     const int k0 = stage * BK;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int blk = wave * 4 + j;
+    for (int j = 0; j < TS / 32; ++j) {
+      const int blk = wave * (TS / 32) + j;
       uint32_t o;
       if (kmaj) {
-        const int k = k0 + 4 * blk + (lane >> 4), c = r0 + 8 * kmaj_chunk(4 * blk + (lane >> 4), lane & 15);
+        const int kr = blk * (64 / CH) + lane / CH, k = k0 + kr, c = r0 + 8 * small_chunk<TS>(kr, lane % CH);
         o = k < p.K && c < rows ? (uint32_t)((k * ld + c) * 2) : kOob;
       } else {
         const int r = blk * 8 + sub, k = k0 + 8 * ((lane & 7) ^ swz(r));
@@ -451,28 +461,28 @@ __global__ __launch_bounds__(256) void moe_orth_tile128_kernel(OrthProduct p) {
     }
   };
   auto issue = [&](int stage, int buf) {
-    char* st = lds + __builtin_amdgcn_readfirstlane(buf * kStage128);
+    char* st = lds + __builtin_amdgcn_readfirstlane(buf * SB);
     issue_op(rsA, KA, t.m0, p.M, p.lda, stage, st);
-    issue_op(rsB, KB, t.n0, p.N, p.ldb, stage, st + kStage128 / 2);
+    issue_op(rsB, KB, t.n0, p.N, p.ldb, stage, st + SB / 2);
   };
   typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
   typedef __attribute__((address_space(3))) char lds_char;
   auto read = [&](const char* st, bool kmaj, int r0, int ks) {
     if (kmaj) {
       const int q = lane & 15, k = 16 * ks + 8 * kh + (q >> 2), c = r0 + 16 * ((lane >> 4) & 1) + 4 * (q & 3);
-      const char* at = st + k * 256 + kmaj_chunk(k, c >> 3) * 16 + (c & 7) * 2;
+      const char* at = st + k * (2 * TS) + small_chunk<TS>(k, c >> 3) * 16 + (c & 7) * 2;
       const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)((lds_char*)at));
-      const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)((lds_char*)(at + 4 * 256)));
+      const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)((lds_char*)(at + 4 * 2 * TS)));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
     const int r = r0 + lr;
     return *reinterpret_cast<const bf16x8*>(st + r * 128 + ((2 * ks + kh) ^ swz(r)) * 16);
   };
-  f32x16 acc[2][2];
+  f32x16 acc[NB][NB];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   const int n = t.s1 - t.s0;
@@ -480,53 +490,55 @@ __global__ __launch_bounds__(256) void moe_orth_tile128_kernel(OrthProduct p) {
   if (n > 1) issue(t.s0 + 1, 1);
   int buf = 0;
   for (int s = 0; s < n; ++s) {
-    if (s + 1 < n)
+    if (s + 1 < n && TS == 128)
       asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // stage s landed, s + 1 may fly
+    else if (s + 1 < n)
+      asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
     else
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();  // every wave's part of stage s; all have left stage s - 1
     asm volatile("" ::: "memory");
     const int b2 = buf == 0 ? 2 : buf - 1;
     if (s + 2 < n) issue(t.s0 + s + 2, b2);
-    const char* sa = lds + buf * kStage128;
-    const char* sb = sa + kStage128 / 2;
+    const char* sa = lds + buf * SB;
+    const char* sb = sa + SB / 2;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
-      bf16x8 a[2], b[2];
+      bf16x8 a[NB], b[NB];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) a[i] = read(sa, KA, wm * 64 + 32 * i, ks);
+      for (int i = 0; i < NB; ++i) a[i] = read(sa, KA, wm * (TS / 2) + 32 * i, ks);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) b[j] = read(sb, KB, wn * 64 + 32 * j, ks);
+      for (int j = 0; j < NB; ++j) b[j] = read(sb, KB, wn * (TS / 2) + 32 * j, ks);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<true>(a[i], b[j], acc[i][j]);
+        for (int j = 0; j < NB; ++j) acc[i][j] = mfma32<true>(a[i], b[j], acc[i][j]);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of stage s are done
     buf = buf == 2 ? 0 : buf + 1;
   }
   if (t.piece >= 0) {
-    float* P = p.partial + (int64_t)t.piece * 16384;
+    float* P = p.partial + (int64_t)t.piece * (TS * TS);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          P[(wm * 64 + 32 * i + 8 * (r >> 2) + 4 * kh + (r & 3)) * 128 + wn * 64 + 32 * j + lr] = acc[i][j][r];
+          P[(wm * (TS / 2) + 32 * i + 8 * (r >> 2) + 4 * kh + (r & 3)) * TS + wn * (TS / 2) + 32 * j + lr] = acc[i][j][r];
     return;
   }
   float* tile = reinterpret_cast<float*>(lds);
-  static_assert(128 * tile_pitch<128>() * 4 <= 3 * kStage128, "the results must fit");
+  static_assert(TS * tile_pitch<TS>() * 4 <= 3 * SB, "the results must fit");
   __syncthreads();  // the last stage's reads are done
-  emit_tile<SYM, 128, 128>(p, (int64_t)t.e * p.M * p.N, t.m0, t.n0, tile, SYM && t.m0 != t.n0, [&](float* d) {
+  emit_tile<SYM, TS, TS>(p, (int64_t)t.e * p.M * p.N, t.m0, t.n0, tile, SYM && t.m0 != t.n0, [&](float* d) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          d[(wm * 64 + 32 * i + 8 * (r >> 2) + 4 * kh + (r & 3)) * tile_pitch<128>() + wn * 64 + 32 * j + lr] =
+          d[(wm * (TS / 2) + 32 * i + 8 * (r >> 2) + 4 * kh + (r & 3)) * tile_pitch<TS>() + wn * (TS / 2) + 32 * j + lr] =
               acc[i][j][r];
   });
 }
@@ -562,8 +574,8 @@ __global__ __launch_bounds__(256) void moe_orth_fixup_kernel(OrthProduct p) {
 // fp16 copy, P and Q in LDS.  A tall matrix is loaded and stored transposed.  Rows and
 // columns past m and n are zeros and stay zeros.  Bound by the chain of products of one
 // tile each and the vector work between them (conversions of up to 128 results per
-// lane): 8 matrices of 256 x 128 take 50 us, in 17 launches 118 us; 3 of 64 x 64 32 us
-// against 88 us.
+// lane): 8 matrices of 256 x 128 take 48 us, in 17 launches of 64 x 64 tiles 67 us;
+// 64 of 128 x 256 47 us against 89 us.
 constexpr int kSmallM = 128, kSmallN = 256;
 constexpr int kPitchX = kSmallN + 8, kPitchP = kSmallM + 8;  // fp16 elements; 16-byte reads of 16 rows spread
 constexpr int kSmallLds = (kSmallM * kPitchX + 2 * kSmallM * kPitchP) * 2 + 64;
@@ -741,12 +753,12 @@ __global__ __launch_bounds__(256) void moe_orth_small_kernel(const void* g, int 
 template <int TS, bool KA, bool KB, bool SYM>
 hipError_t launch_tiles(const OrthProduct& p, hipStream_t s) {
   static std::atomic<uint64_t> done;
-  constexpr int lds = TS == 256 ? kLdsBytes : 3 * kStage128;
+  constexpr int lds = TS == 256 ? kLdsBytes : 3 * small_stage_bytes<TS>();
   void (*kernel)(OrthProduct);
   if constexpr (TS == 256)
     kernel = moe_orth_tile256_kernel<KA, KB, SYM>;
   else
-    kernel = moe_orth_tile128_kernel<KA, KB, SYM>;
+    kernel = moe_orth_tile_kernel<TS, KA, KB, SYM>;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), lds, done);
   if (e != hipSuccess) return e;
   const int64_t blocks = (p.n_dp + 7) / 8 * 8 + (int64_t)p.R * p.S;
@@ -765,10 +777,13 @@ hipError_t launch_product(OrthProduct p, int E, int ctas, hipStream_t s) {
     p.per = SYM ? p.tm * (p.tm + 1) / 2 : p.tm * p.tn;
     return (int64_t)E * p.per;
   };
-  // half the chip's CUs with 256 x 256 tiles, or smaller ones that reach more CUs
+  // half the chip's CUs with 256 x 256 tiles, or smaller ones that reach more CUs; 64 x 64
+  // where 128 x 128 do not reach all (8 matrices of 512 x 512 160 us against 235, 2 of
+  // 400 x 392 102 against 178; where the chip is filled they have half the reuse)
   int64_t V = tiles(256);
-  const int ts = V * 2 >= ctas ? 256 : 128;
-  if (ts == 128) V = tiles(128);
+  int ts = 256;
+  if (V * 2 < ctas) V = tiles(ts = 128);
+  if (ts == 128 && V < ctas) V = tiles(ts = 64);
   // the partial last round, cut along K in pieces of at least 4 stages
   const int64_t rounds = V / ctas;
   int64_t R = V % ctas;
@@ -780,7 +795,8 @@ hipError_t launch_product(OrthProduct p, int E, int ctas, hipStream_t s) {
   p.n_dp = V - R;
   p.R = (int)R;
   p.S = (int)S;
-  return ts == 256 ? launch_tiles<256, KA, KB, SYM>(p, s) : launch_tiles<128, KA, KB, SYM>(p, s);
+  if (ts == 64) return launch_tiles<64, KA, KB, SYM>(p, s);
+  return ts == 128 ? launch_tiles<128, KA, KB, SYM>(p, s) : launch_tiles<256, KA, KB, SYM>(p, s);
 }
 
 }  // namespace

@@ -1,3 +1,6 @@
+// The 16 / 32-row tiles that stream weights: gemm_decode.hip describes them.  A
+// parameter block P says whether the groups come padded to tiles (the layer) or by
+// offsets on the device (grouped.hip).
 #pragma once
 #include <type_traits>
 

@@ -1,3 +1,10 @@
+// The 256 x 256 x 64 tile on MFMA: K loop, schedule, cut last round and its finish,
+// and the weight gradients' tiles.  gemm_prefill.hip describes its layouts for the
+// layer's products; a parameter block P says what else a product is: kRagged (groups
+// given by offsets on the device, rows in place), kFold (short last tiles ride along
+// with the tile before), kLora (adapters' second product added to the sums), out16 and
+// stream_out (how results leave).  Used by gemm_prefill.hip, grouped_prefill.hip,
+// grouped_wgrad.hip, lora_prefill.hip and orthogonalize.hip.
 #pragma once
 #include <type_traits>
 

@@ -139,7 +139,8 @@ __global__ __launch_bounds__(256) void moe_lora_wgrad_kernel(LoraWgrad p) {
     }
   }
   // lane (col, gq) holds ranks 16 b + 4 gq + i of column c0 + 32 wave + 16 j + col
-  const float sc = which ? (p.scale ? p.scale[l] : 1.f) : 1.f;
+  // (without rows the scale is not read: a NaN there would reach the zeros)
+  const float sc = which && p.scale && rows > 0 ? p.scale[l] : 1.f;
   float* out = (which ? p.out[1] : p.out[0]) + (int64_t)l * r * C;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {

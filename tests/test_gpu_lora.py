@@ -116,6 +116,24 @@ def test_no_scale(T):
     check(T, 128, 136, 3, 16, "runs", scale=False)
 
 
+@pytest.mark.parametrize("T", [1, 20, 100, 300])
+def test_nothing_of_an_unnamed_adapter_is_read(T):
+    """Not its scale either: gradients of adapters without rows are zeros."""
+    D, N, L, r = 72, 136, 6, 8
+    m = {k: v.to(DEV) for k, v in make(T, D, N, L, r).items()}
+    ad = (torch.arange(T, dtype=torch.int32, device=DEV) % 3) * 2  # 0, 2, 4
+    for l in range(L):
+        if l not in set(ad.tolist()):
+            m["a"][l] = m["b"][l] = m["scale"][l] = float("nan")
+    xa = torch.empty((T, r), device=DEV)
+    y = moe.moe_lora_forward(m["x"], m["w"], m["a"], m["b"], ad, m["scale"], xa=xa)
+    g = moe.moe_lora_backward(m["x"], m["w"], m["a"], m["b"], ad, m["dy"], xa, m["scale"])
+    assert all(torch.isfinite(v).all() for v in (y, xa, g["dx"], g["da"], g["db"]))
+    for l in range(L):
+        if l not in set(ad.tolist()):
+            assert (g["da"][l] == 0).all() and (g["db"][l] == 0).all()
+
+
 @pytest.mark.parametrize("T", [64, 600])
 def test_many_adapters(T):
     check(T, 72, 80, 256, 8, "mixed", out=torch.float32)

@@ -1,4 +1,5 @@
-// The adapters' products for few rows (lora_few_rows in ops_plan.hpp): two launches.
+// The adapters' products for few rows (lora_few_rows in ops_plan.hpp says which calls):
+// two launches.
 //
 // First, in one launch: the projection's weights are streamed once (tiles of up to 64
 // rows x 64 columns, K cut into parts so that the grid fills the chip, fp32 partial

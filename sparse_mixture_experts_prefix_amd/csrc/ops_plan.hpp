@@ -34,13 +34,16 @@ int check_lora_tensors(const moe_lora_shape* s, const moe_lora_tensors* t);
 
 // Whether a call takes the few-row path: its second product reads an adapter's rows
 // once per row that names it (2 N r bytes), whoever its neighbours are, where the
-// 256-row tiles take a stage of each adapter they hold.  N = D = 4096, few rows against
-// tiles: 250 rows of 30 adapters, rank 64 67 us against 208, rank 128 96 against 371;
-// of 2 adapters, rank 64 54 against 52, rank 128 77 against 63; 100 rows of 2 adapters,
-// rank 128 41 against 53.  How many adapters the rows name is known on the device
-// alone: L bounds it.
+// 256-row tiles take a stage of each adapter they hold.  Few rows against tiles, N = D =
+// 4096: 250 rows of 30 adapters, rank 64 67 us against 208, rank 128 96 against 371; of 2
+// adapters, rank 64 54 against 52, rank 128 77 against 63; 100 rows of 2 adapters, rank 128
+// 41 against 53; 512 rows, rank 16, of 30 adapters 62 against 132, of 2 56 against 66;
+// past the limits, 1024 rows of 2 adapters, rank 32, 120 against 80.  How many adapters
+// the rows name is known on the device alone: L bounds it.
 inline bool lora_few_rows(const moe_lora_shape* s) {
-  return s->T <= 64 || (s->T <= 256 && (s->L > 4 || s->T * s->r <= 16384));
+  const int64_t T = s->T, Tr = T * s->r;
+  if (T <= 64 || (T <= 256 && (s->L > 4 || Tr <= 16384))) return true;
+  return s->L > 4 && T <= 1024 && Tr <= 32768 && T * s->N * s->D <= int64_t(1) << 33;
 }
 
 struct LoraPlan {

@@ -98,6 +98,15 @@ def test_more_rows_than_a_tile_of_64(T, L, r, kind):
     check(T, 264, 1096, L, r, kind, out=torch.float32, seed=T)
 
 
+@pytest.mark.parametrize("T,L,r", [(257, 30, 120), (300, 30, 128), (513, 6, 64), (600, 30, 64), (1024, 5, 32),
+                                   (1025, 5, 32), (1100, 256, 8), (1100, 40, 16)])
+@pytest.mark.parametrize("kind", ["mixed", "runs"])
+def test_many_adapters_in_a_tile_of_256_rows(T, L, r, kind):
+    """Both sides of that choice for more rows; tiles that hold 2 to 256 adapters."""
+    check(T, 136, 264, L, r, kind, seed=r)
+    check(T, 264, 136, L, r, kind, out=torch.float32, seed=T)
+
+
 @pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 64, 72, 128])
 @pytest.mark.parametrize("T", [9, 300])
 def test_ranks(T, r):

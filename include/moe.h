@@ -338,7 +338,10 @@ int moe_backward_saved(const moe_shape* shape, const moe_weights* w, const int32
  * hold: contiguous row-major device tensors, 16-byte aligned pointers (4-byte
  * where said), the caller's stream and buffers, host checks before the first
  * launch, no host synchronisation, no memory kept between calls.  Outputs
- * must not overlap inputs, the workspace or each other.
+ * must not overlap inputs, the workspace or each other.  A workspace size is that
+ * of its own shape: fewer rows can need more (other kernels), so a buffer for
+ * several shapes takes the largest of their sizes.  Calls that may run at the same
+ * time, captured graphs among them, need workspaces of their own.
  * ------------------------------------------------------------------------ */
 
 /* Element types of outputs (any other value: MOE_ERR_INVALID_ARG) */

@@ -5,7 +5,10 @@
 //
 // Many rows per group: the 256 x 256 x 64 tiles of gemm_tile.hpp, MFMA-bound.
 // Few (mostly one K stage): 128 x 128 tiles, of which two share a CU, so that one's
-// stores overlap the other's loads and products.  Up to a few hundred rows the time
+// stores overlap the other's loads and products.  Also where 256 x 256 tiles would
+// leave half the CUs idle: a tile walks its group's rows alone, the smaller one in
+// less time (2 groups of 4367 rows, 216 x 128: 60 us against 105; 4 of 2048 rows, 1024 x
+// 1024: 41 against 65; with 160 tiles, 10 of 205 rows, 18.4 against 17.4).  Up to a few hundred rows the time
 // is the gradient's stores (4 G N K bytes).  They are non-temporal (nothing of a
 // gradient this size stays in a cache: 541 -> 449 us for 64 x 2048 x 4096 at 156 rows
 // each, held in a cache), and the tiles go in row order, so that what the chip stores
@@ -136,10 +139,14 @@ __global__ __launch_bounds__(256) void moe_grouped_wgrad_small_kernel(RaggedWgra
 hipError_t launch_grouped_wgrad(const moe_gemm_shape& s, const void* dy, const void* x,
                                 const int32_t* offsets, float* dw, hipStream_t st) {
   static std::atomic<uint64_t> done[2];
-  const bool small = (int64_t)s.R <= (int64_t)kWgradSmallRows * s.G;
+  int ctas = 0;
+  hipError_t e = split_ctas(&ctas);
+  if (e != hipSuccess) return e;
+  const int64_t large = (int64_t)s.G * ((s.N + BM - 1) / BM) * ((s.K + BM - 1) / BM);
+  const bool small = (int64_t)s.R <= (int64_t)kWgradSmallRows * s.G || large * 2 <= ctas;
   const int ts = small ? 128 : BM, lds = small ? kSmallLds : kLdsBytes;
   void (*kernel)(RaggedWgrad) = small ? moe_grouped_wgrad_small_kernel : moe_grouped_wgrad_kernel;
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), lds, done[small]);
+  e = allow_lds(reinterpret_cast<const void*>(kernel), lds, done[small]);
   if (e != hipSuccess) return e;
   RaggedWgrad p{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x), s.N, s.K, s.N, s.K,
                 s.G, offsets, s.R, dw, (s.N + ts - 1) / ts, (s.K + ts - 1) / ts};

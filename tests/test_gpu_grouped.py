@@ -184,6 +184,13 @@ def test_wgrad_many_groups():
     check_wgrad(torch.randint(0, 9, (256,), generator=g).tolist(), 24, 40)
 
 
+@pytest.mark.parametrize("sizes,N,K", [([2000], 264, 136), ([1500, 0, 701, 33], 72, 520), ([1, 640, 129], 136, 136),
+                                       ([300] * 9, 1032, 1032), ([513, 0, 129, 777], 1544, 1544)])
+def test_wgrad_few_and_many_tiles(sizes, N, K):
+    """Both sides of the choice of tiles by how many there are, over many rows."""
+    check_wgrad(sizes, N, K, seed=N)
+
+
 def test_no_rows():
     x = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
     w = normal((2, 32, 64), 0).to(DEV)
